@@ -821,6 +821,16 @@ double wave_efficiency(int tiles, int pairs) {
 
 }  // namespace
 
+int gemm_variant_now() {
+  if (g_variant < 0) {
+    const char* e = getenv("MT_GEMM_VARIANT");
+    g_variant = (e && !strcmp(e, "single")) ? 1 : (e && !strcmp(e, "pair")) ? 2 : 0;
+  }
+  return g_variant;
+}
+
+uint64_t gemm_wait_limit_now() { return g_wait_ns; }
+
 int gemm_bf16(const GemmDesc& g, cudaStream_t st, int* err) {
   if (g.M <= 0 || g.N <= 0 || g.K <= 0) return (g.M == 0 || g.N == 0) ? MT_OK : MT_ERR_ARG;
   if (!g.A || !g.B || !g.C) return MT_ERR_ARG;
@@ -839,10 +849,7 @@ int gemm_bf16(const GemmDesc& g, cudaStream_t st, int* err) {
     cudaDeviceGetAttribute(&g_num_sms, cudaDevAttrMultiProcessorCount, dev);
     if (g_num_sms <= 0) return MT_ERR_CUDA;
   }
-  if (g_variant < 0) {
-    const char* e = getenv("MT_GEMM_VARIANT");
-    g_variant = (e && !strcmp(e, "single")) ? 1 : (e && !strcmp(e, "pair")) ? 2 : 0;
-  }
+  gemm_variant_now();
   // CTA pairs (256-row tiles) when the pair tiles fill every SM pair at least
   // once; the pair tile's width is 256 unless 128 quantizes into waves clearly
   // better. Small problems use the single-CTA kernel.

@@ -1,4 +1,5 @@
 // C-ABI entry points of the individual kernels (declared in mt_kernels.h).
+#include "act_dropout.cuh"
 #include "mt_internal.h"
 #include "mt_kernels.h"
 
@@ -164,4 +165,142 @@ extern "C" int mt_k_attn_bwd_tc(const void* q, const void* k, const void* v, int
   a.lddkv = lddkv; a.b = b; a.s = s; a.H = H; a.Hkv = Hkv; a.hd = hd; a.scale = 1.0f / std::sqrt((float)hd);
   a.rope_cos = cos_tab; a.rope_sin = sin_tab;
   return mt::attention_bwd_tc(a, S(stream), dev_err);
+}
+
+// ---------------------------------------------------------------------------
+// Layer norm, dropout, linear layers with an epilogue, gated feed-forward.
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int kMostSize = 1 << 30;
+
+bool size_ok(int n) { return n >= 0 && n <= kMostSize; }
+bool type_ok(int t) { return t == MT_F32 || t == MT_BF16; }
+bool act_ok(int a) { return a >= MT_ACT_NONE && a <= MT_ACT_SILU; }
+// A matrix operand: present, aligned, its pitch a multiple of 16 bytes and no shorter than a row.
+bool mat_ok(const void* p, int type, int64_t ld, int64_t width) {
+  return p && al16(p) && ld >= width && ld % (type == MT_F32 ? 4 : 8) == 0;
+}
+bool opt_mat_ok(const void* p, int type, int64_t ld, int64_t width) { return !p || mat_ok(p, type, ld, width); }
+
+// The launchers' dropout; rows: of the call. offset_dev is read as 8 bytes.
+int drop_of(const mt_dropout* d, int rows, mt::DropDesc* out) {
+  if (d && (reinterpret_cast<uintptr_t>(d->offset_dev) & 7)) return MT_ERR_ARG;
+  return mt::make_drop(d, rows, out);
+}
+
+}  // namespace
+
+extern "C" int mt_k_layernorm_fwd(const void* x, int x_type, int64_t ldx, const void* g, const void* b, void* y,
+                                  int y_type, int64_t ldy, float* mean, float* rstd, int T, int d, float eps,
+                                  void* stream) {
+  if (!type_ok(x_type) || !type_ok(y_type) || !size_ok(T) || d <= 0 || !(eps >= 0.f)) return MT_ERR_ARG;
+  if (d > 8192) return MT_ERR_CONFIG;
+  if (T == 0) return MT_OK;
+  if (!mat_ok(x, x_type, ldx, d) || !mat_ok(y, y_type, ldy, d) || !g || !al16(g) || !al16(b)) return MT_ERR_ARG;
+  return mt::launch_layernorm_fwd(x, x_type, ldx, g, b, y, y_type, ldy, mean, rstd, T, d, eps, S(stream));
+}
+
+extern "C" size_t mt_k_layernorm_bwd_partial_floats(int T, int d) {
+  return size_ok(T) && d > 0 && d <= 8192 ? mt::layernorm_bwd_partial_floats(T, d) : 0;
+}
+
+extern "C" int mt_k_layernorm_bwd(const void* x, int x_type, int64_t ldx, const void* g, const float* mean,
+                                  const float* rstd, const void* dy, int dy_type, int64_t lddy, const void* dres,
+                                  int64_t lddres, void* dx, void* dx_bf16, int64_t lddx, float* part, float* dg,
+                                  float* db, int T, int d, void* stream) {
+  if (!type_ok(x_type) || !type_ok(dy_type) || !size_ok(T) || d <= 0 || !dg) return MT_ERR_ARG;
+  if (d > 8192) return MT_ERR_CONFIG;
+  if (T > 0) {
+    if (!mat_ok(x, x_type, ldx, d) || !mat_ok(dy, dy_type, lddy, d) || !opt_mat_ok(dres, x_type, lddres, d) ||
+        !mat_ok(dx, x_type, lddx, d) || !g || !al16(g) || !mean || !rstd || !part)
+      return MT_ERR_ARG;
+    if (dx_bf16 && (x_type != MT_F32 || !mat_ok(dx_bf16, MT_BF16, lddx, d))) return MT_ERR_ARG;
+  }
+  const mt::LayerNormBwd a{x,      x_type, ldx, g,       mean, rstd, dy, dy_type, lddy, dres,
+                           lddres, dx,     dx_bf16, lddx, part, dg,   db, T,       d};
+  return mt::launch_layernorm_bwd(a, S(stream));
+}
+
+extern "C" int mt_k_dropout(const void* x, int x_type, int64_t ldx, const mt_dropout* drop, const void* res,
+                            int64_t ldr, void* y, int y_type, int64_t ldy, int T, int d, void* stream) {
+  mt::DropDesc dd;
+  if (!type_ok(x_type) || !type_ok(y_type) || !size_ok(T) || !size_ok(d)) return MT_ERR_ARG;
+  if (const int rc = drop_of(drop, T, &dd)) return rc;
+  if (T == 0 || d == 0) return MT_OK;
+  if (!mat_ok(x, x_type, ldx, d) || !mat_ok(y, y_type, ldy, d) || !opt_mat_ok(res, y_type, ldr, d)) return MT_ERR_ARG;
+  return mt::launch_dropout(x, x_type, ldx, dd, res, ldr, y, y_type, ldy, T, d, S(stream));
+}
+
+extern "C" int mt_k_linear_fwd(const void* A, int64_t lda, const void* W, int64_t ldw, const void* bias, int act,
+                               const mt_dropout* drop, const void* R, int64_t ldr, void* Z, int64_t ldz, void* C,
+                               int out_type, int64_t ldc, int M, int N, int K, void* stream, int32_t* dev_err) {
+  mt::DropDesc dd;
+  if (!type_ok(out_type) || !act_ok(act) || !size_ok(M) || !size_ok(N) || !size_ok(K)) return MT_ERR_ARG;
+  if (const int rc = drop_of(drop, M, &dd)) return rc;
+  if (M == 0 || N == 0) return MT_OK;
+  if (K == 0 || !mat_ok(A, MT_BF16, lda, K) || !mat_ok(W, MT_BF16, ldw, K) || !al16(bias) ||
+      !opt_mat_ok(R, out_type, ldr, N) || !opt_mat_ok(Z, MT_BF16, ldz, N) || !mat_ok(C, out_type, ldc, N))
+    return MT_ERR_ARG;
+  const mt::LinearFwd a{A, lda, W, ldw, bias, act, R, ldr, Z, ldz, C, out_type, ldc, M, N, K};
+  return mt::launch_linear_fwd(a, dd, S(stream), dev_err);
+}
+
+extern "C" size_t mt_k_linear_bwd_act_partial_floats(int M, int N) {
+  return size_ok(M) && size_ok(N) ? mt::linear_bwd_partial_floats(M, N) : 0;
+}
+
+extern "C" int mt_k_linear_bwd_act(const void* dY, int64_t lddy, const void* W, int64_t ldw, const void* Z, int64_t ldz,
+                                   int act, const mt_dropout* drop, void* dZ, int64_t lddz, float* part, float* db,
+                                   int M, int N, int K, void* stream, int32_t* dev_err) {
+  mt::DropDesc dd;
+  if (!act_ok(act) || !size_ok(M) || !size_ok(N) || !size_ok(K)) return MT_ERR_ARG;
+  if (const int rc = drop_of(drop, M, &dd)) return rc;
+  if (N == 0) return MT_OK;
+  if (M == 0) return !db || cudaMemsetAsync(db, 0, sizeof(float) * N, S(stream)) == cudaSuccess ? MT_OK : MT_ERR_CUDA;
+  if (K == 0 || !mat_ok(dY, MT_BF16, lddy, K) || !mat_ok(W, MT_BF16, ldw, N) || !opt_mat_ok(Z, MT_BF16, ldz, N) ||
+      !mat_ok(dZ, MT_BF16, lddz, N) || (act != MT_ACT_NONE && !Z) || (db && !part))
+    return MT_ERR_ARG;
+  const mt::LinearBwd a{dY, lddy, W, ldw, Z, ldz, act, dZ, lddz, part, db, M, N, K};
+  return mt::launch_linear_bwd_act(a, dd, S(stream), dev_err);
+}
+
+extern "C" size_t mt_k_act_bwd_partial_floats(int M, int N) {
+  return size_ok(M) && size_ok(N) ? mt::act_bwd_partial_floats(M, N) : 0;
+}
+
+extern "C" int mt_k_act_bwd(const void* dC, int dc_type, int64_t lddc, const void* Z, int64_t ldz, int act,
+                            const mt_dropout* drop, void* dZ, int64_t lddz, float* part, float* db, int M, int N,
+                            void* stream) {
+  mt::DropDesc dd;
+  if (!type_ok(dc_type) || !act_ok(act) || !size_ok(M) || !size_ok(N)) return MT_ERR_ARG;
+  if (const int rc = drop_of(drop, M, &dd)) return rc;
+  if (M > 0 && N > 0 &&
+      (!mat_ok(dC, dc_type, lddc, N) || !opt_mat_ok(Z, MT_BF16, ldz, N) || !mat_ok(dZ, MT_BF16, lddz, N) ||
+       (act != MT_ACT_NONE && !Z) || (db && !part)))
+    return MT_ERR_ARG;
+  return mt::launch_act_bwd(dC, dc_type, lddc, Z, ldz, act, dd, dZ, lddz, part, db, M, N, S(stream));
+}
+
+extern "C" int mt_k_gated_ffn_fwd(const void* x, int64_t ldx, const void* Wgu, int64_t ldw, int act, void* gu,
+                                  int64_t ldgu, void* h, int64_t ldh, int M, int F, int K, void* stream,
+                                  int32_t* dev_err) {
+  if (!act_ok(act) || !size_ok(M) || !size_ok(F) || !size_ok(K) || (F % 8)) return MT_ERR_ARG;
+  if (M == 0 || F == 0) return MT_OK;
+  if (K == 0 || !mat_ok(x, MT_BF16, ldx, K) || !mat_ok(Wgu, MT_BF16, ldw, K) ||
+      !opt_mat_ok(gu, MT_BF16, ldgu, 2 * (int64_t)F) || !mat_ok(h, MT_BF16, ldh, F))
+    return MT_ERR_ARG;
+  return mt::launch_gated_ffn_fwd(x, ldx, Wgu, ldw, act, gu, ldgu, h, ldh, M, F, K, S(stream), dev_err);
+}
+
+extern "C" int mt_k_gated_ffn_bwd(const void* dy, int64_t lddy, const void* Wd, int64_t ldw, const void* gu,
+                                  int64_t ldgu, int act, void* dgu, int64_t lddgu, void* h, int64_t ldh, int M, int F,
+                                  int K, void* stream, int32_t* dev_err) {
+  if (!act_ok(act) || !size_ok(M) || !size_ok(F) || !size_ok(K) || (F % 8)) return MT_ERR_ARG;
+  if (M == 0 || F == 0) return MT_OK;
+  if (K == 0 || !mat_ok(dy, MT_BF16, lddy, K) || !mat_ok(Wd, MT_BF16, ldw, F) ||
+      !mat_ok(gu, MT_BF16, ldgu, 2 * (int64_t)F) || !mat_ok(dgu, MT_BF16, lddgu, 2 * (int64_t)F) ||
+      !opt_mat_ok(h, MT_BF16, ldh, F))
+    return MT_ERR_ARG;
+  return mt::launch_gated_ffn_bwd(dy, lddy, Wd, ldw, gu, ldgu, act, dgu, lddgu, h, ldh, M, F, K, S(stream), dev_err);
 }

@@ -1,0 +1,309 @@
+// Layer norm of a row, forward and backward (sm_100a):
+//   y_j  = (x_j - m) r g_j + b_j,  m = mean x,  r = (mean (x - m)^2 + eps)^-1/2
+// and, with w_j = dy_j g_j and xh_j = (x_j - m) r,
+//   dx_j = dres_j + r (w_j - mean w - xh_j mean(w xh))
+//   dg_j = sum over rows of dy_j xh_j,  db_j = sum over rows of dy_j.
+// Both passes are bound by device memory: each reads its inputs once into
+// registers, where the row's two statistics are taken in fp32 (the variance
+// from the centred values, so that a large mean costs no digits).
+#include "act_dropout.cuh"
+
+namespace mt {
+
+namespace {
+
+// Sum of (a, b) over the TX threads of a row piece; TX a multiple of 32. The
+// block holds RY = blockDim.x / TX such rows; `red` has 2 * blockDim.x / 32
+// floats. Every thread of the block calls it.
+template <int TX>
+__device__ __forceinline__ float2 row_sum2(float a, float b, float* red) {
+  a = warp_sum(a);
+  b = warp_sum(b);
+  if (TX == 32) return make_float2(a, b);
+  const int warp = threadIdx.x >> 5;
+  if ((threadIdx.x & 31) == 0) {
+    red[2 * warp] = a;
+    red[2 * warp + 1] = b;
+  }
+  __syncthreads();
+  constexpr int W = TX / 32;
+  const int w0 = warp / W * W;
+  float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    s.x += red[2 * (w0 + i)];
+    s.y += red[2 * (w0 + i) + 1];
+  }
+  return s;
+}
+
+// Forward: TX threads to a row (a warp up to 2048 columns, 256 threads above),
+// G pieces of eight columns to a thread.
+template <typename X, typename Y, int TX, int G>
+__global__ void __launch_bounds__(256) k_layernorm_fwd(const X* __restrict__ x, int64_t ldx, const bf16* __restrict__ g,
+                                                       const bf16* __restrict__ b, Y* __restrict__ y, int64_t ldy,
+                                                       float* __restrict__ mean, float* __restrict__ rstd, int T, int d,
+                                                       float eps) {
+  __shared__ float red[2][16];
+  const int64_t row = (int64_t)blockIdx.x * (256 / TX) + threadIdx.x / TX;
+  const int tx = threadIdx.x % TX;
+  const bool ok = row < T;
+  if (TX == 32 && !ok) return;  // no barrier below; wider rows have one row to a block
+  const X* xr = x + row * ldx;
+  float v[G][8];
+  float s = 0.f;
+#pragma unroll
+  for (int k = 0; k < G; ++k) {
+    const int c = (tx + k * TX) * 8;
+    load8n(xr + c, d - c, v[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < G; ++k)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s += v[k][e];
+  const float m = row_sum2<TX>(s, 0.f, red[0]).x / (float)d;
+  float q = 0.f;
+#pragma unroll
+  for (int k = 0; k < G; ++k) {
+    const int n = d - (tx + k * TX) * 8;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float t = e < n ? v[k][e] - m : 0.f;
+      q += t * t;
+    }
+  }
+  const float r = rsqrtf(row_sum2<TX>(q, 0.f, red[1]).x / (float)d + eps);
+#pragma unroll
+  for (int k = 0; k < G; ++k) {
+    const int c = (tx + k * TX) * 8;
+    if (c >= d) continue;
+    float gv[8], bv[8];
+    load8n(g + c, d - c, gv);
+    if (b) {
+      load8n(b + c, d - c, bv);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) bv[e] = 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[k][e] = (v[k][e] - m) * r * gv[e] + bv[e];
+    store8n(y + row * ldy + c, d - c, v[k]);
+  }
+  if (tx == 0) {
+    if (mean) mean[row] = m;
+    if (rstd) rstd[row] = r;
+  }
+}
+
+// Backward: a block of 256 threads takes a run of rows, RY = 256 / TX at a
+// time; a thread keeps its columns' sums of dg and db over all of them. The
+// block's sums go to its own row [dg | db] of `part`.
+template <typename X, typename Y, int TX, int G>
+__global__ void __launch_bounds__(256) k_layernorm_bwd(const X* __restrict__ x, int64_t ldx, const bf16* __restrict__ g,
+                                                       const float* __restrict__ mean, const float* __restrict__ rstd,
+                                                       const Y* __restrict__ dy, int64_t lddy, const X* dres,
+                                                       int64_t lddres, X* dx, bf16* dx_bf16, int64_t lddx,
+                                                       float* __restrict__ part, int T, int d, int rows_per_block) {
+  constexpr int RY = 256 / TX;
+  __shared__ float red[2][16];
+  __shared__ float col[RY > 1 ? RY - 1 : 1][RY > 1 ? TX * G * 8 : 1];
+  const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
+  float ag[G][8], ab[G][8];
+  uint4 gp[G];
+#pragma unroll
+  for (int k = 0; k < G; ++k) {
+    const int c = (tx + k * TX) * 8;
+    float gv[8];
+    load8n(g + c, d - c, gv);
+    gp[k] = pack8(gv);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ag[k][e] = ab[k][e] = 0.f;
+  }
+  const int64_t r0 = (int64_t)blockIdx.x * rows_per_block;
+  const int64_t r1 = min((int64_t)T, r0 + rows_per_block);
+  int half = 0;
+  for (int64_t base = r0; base < r1; base += RY, half ^= 1) {
+    const int64_t row = base + ty;
+    const bool ok = row < r1;
+    float xv[G][8], dv[G][8], rv[G][8];
+    const float m = ok ? mean[row] : 0.f, r = ok ? rstd[row] : 0.f;
+#pragma unroll
+    for (int k = 0; k < G; ++k) {
+      const int c = (tx + k * TX) * 8, n = ok ? d - c : 0;
+      load8n(x + row * ldx + c, n, xv[k]);
+      load8n(dy + row * lddy + c, n, dv[k]);
+      if (dres) load8n(dres + row * lddres + c, n, rv[k]);
+    }
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int k = 0; k < G; ++k) {
+      const int n = d - (tx + k * TX) * 8;
+      float gv[8];
+      unpack8(gp[k], gv);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float xh = ok && e < n ? (xv[k][e] - m) * r : 0.f;
+        const float w = dv[k][e] * gv[e];
+        xv[k][e] = xh;
+        s1 += w;
+        s2 += w * xh;
+        ag[k][e] += dv[k][e] * xh;
+        ab[k][e] += dv[k][e];
+      }
+    }
+    const float2 s = row_sum2<TX>(s1, s2, red[half]);  // the halves alternate: one barrier a row
+    const float m1 = s.x / (float)d, m2 = s.y / (float)d;
+    if (ok) {
+#pragma unroll
+      for (int k = 0; k < G; ++k) {
+        const int c = (tx + k * TX) * 8;
+        if (c >= d) continue;
+        float gv[8], o[8];
+        unpack8(gp[k], gv);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          o[e] = r * (dv[k][e] * gv[e] - m1 - xv[k][e] * m2);
+          if (dres) o[e] += rv[k][e];
+        }
+        store8n(dx + row * lddx + c, d - c, o);
+        if (dx_bf16) store8n(dx_bf16 + row * lddx + c, d - c, o);
+      }
+    }
+  }
+  // The RY rows' sums meet in shared memory, in the order of ty: dg, then db.
+  float* out = part + (int64_t)blockIdx.x * 2 * d;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    float(&acc)[G][8] = which ? ab : ag;
+    if (RY > 1) {
+      __syncthreads();
+      if (ty > 0) {
+#pragma unroll
+        for (int k = 0; k < G; ++k)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) col[ty - 1][(k * 8 + e) * TX + tx] = acc[k][e];
+      }
+      __syncthreads();
+    }
+    if (ty == 0) {
+#pragma unroll
+      for (int k = 0; k < G; ++k) {
+        const int c = (tx + k * TX) * 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float s = acc[k][e];
+#pragma unroll
+          for (int i = 0; i < RY - 1; ++i) s += col[i][(k * 8 + e) * TX + tx];
+          if (c + e < d) out[which * d + c + e] = s;
+        }
+      }
+    }
+  }
+}
+
+// out[j] = sum over r of part[r, j], 32 columns to a block; thread row y takes
+// the partials y, y + 32, ... and the 32 sums meet in a fixed tree.
+__global__ void __launch_bounds__(1024) k_column_sums(const float* __restrict__ part, int rows, int64_t pitch, int n,
+                                                      float* __restrict__ out, int n1, float* __restrict__ out2) {
+  __shared__ float sh[32][33];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int j = blockIdx.x * 32 + x;
+  float s = 0.f;
+  if (j < n) {
+#pragma unroll 4
+    for (int r = y; r < rows; r += 32) s += part[(int64_t)r * pitch + j];
+  }
+  sh[y][x] = s;
+  __syncthreads();
+  const float t = warp_sum(sh[x][y]);  // warp y now holds column y's 32 sums
+  const int o = blockIdx.x * 32 + y;
+  if (x == 0 && o < n) {
+    if (o < n1)
+      out[o] = t;
+    else if (out2)
+      out2[o - n1] = t;
+  }
+}
+
+constexpr int kLnMaxBlocks = 592;
+
+int ln_bwd_blocks(int T) { return T < kLnMaxBlocks ? (T > 0 ? T : 1) : kLnMaxBlocks; }
+
+template <typename X, typename Y, int TX, int G>
+int ln_fwd_launch(const void* x, int64_t ldx, const void* g, const void* b, void* y, int64_t ldy, float* mean,
+                  float* rstd, int T, int d, float eps, cudaStream_t st) {
+  const int rpb = 256 / TX;
+  k_layernorm_fwd<X, Y, TX, G><<<(T + rpb - 1) / rpb, 256, 0, st>>>((const X*)x, ldx, (const bf16*)g, (const bf16*)b,
+                                                                  (Y*)y, ldy, mean, rstd, T, d, eps);
+  return launch_status();
+}
+
+template <typename X, typename Y>
+int ln_fwd(const void* x, int64_t ldx, const void* g, const void* b, void* y, int64_t ldy, float* mean, float* rstd,
+           int T, int d, float eps, cudaStream_t st) {
+#define MT_LN_FWD(TX, G) return ln_fwd_launch<X, Y, TX, G>(x, ldx, g, b, y, ldy, mean, rstd, T, d, eps, st)
+  if (d <= 256) MT_LN_FWD(32, 1);
+  if (d <= 512) MT_LN_FWD(32, 2);
+  if (d <= 1024) MT_LN_FWD(32, 4);
+  if (d <= 2048) MT_LN_FWD(32, 8);
+  if (d <= 4096) MT_LN_FWD(256, 2);
+  if (d <= 6144) MT_LN_FWD(256, 3);
+  MT_LN_FWD(256, 4);
+#undef MT_LN_FWD
+}
+
+template <typename X, typename Y, int TX, int G>
+int ln_bwd_launch(const LayerNormBwd& a, cudaStream_t st) {
+  const int nb = ln_bwd_blocks(a.T);
+  const int rpb = (a.T + nb - 1) / nb;
+  k_layernorm_bwd<X, Y, TX, G><<<nb, 256, 0, st>>>((const X*)a.x, a.ldx, (const bf16*)a.g, a.mean, a.rstd,
+                                                   (const Y*)a.dy, a.lddy, (const X*)a.dres, a.lddres, (X*)a.dx,
+                                                   (bf16*)a.dx_bf16, a.lddx, a.part, a.T, a.d, rpb);
+  if (const int rc = launch_status()) return rc;
+  return launch_column_sums(a.part, nb, 2 * (int64_t)a.d, 2 * a.d, a.dg, a.d, a.db, st);
+}
+
+template <typename X, typename Y>
+int ln_bwd(const LayerNormBwd& a, cudaStream_t st) {
+  if (a.d <= 256) return ln_bwd_launch<X, Y, 32, 1>(a, st);
+  if (a.d <= 512) return ln_bwd_launch<X, Y, 64, 1>(a, st);
+  if (a.d <= 1024) return ln_bwd_launch<X, Y, 128, 1>(a, st);
+  if (a.d <= 2048) return ln_bwd_launch<X, Y, 256, 1>(a, st);
+  if (a.d <= 4096) return ln_bwd_launch<X, Y, 256, 2>(a, st);
+  if (a.d <= 6144) return ln_bwd_launch<X, Y, 256, 3>(a, st);
+  return ln_bwd_launch<X, Y, 256, 4>(a, st);
+}
+
+}  // namespace
+
+int launch_column_sums(const float* part, int rows, int64_t pitch, int n, float* out, int n1, float* out2,
+                       cudaStream_t st) {
+  if (n <= 0) return MT_OK;
+  k_column_sums<<<(n + 31) / 32, 1024, 0, st>>>(part, rows, pitch, n, out, n1, out2);
+  return launch_status();
+}
+
+int launch_layernorm_fwd(const void* x, int x_type, int64_t ldx, const void* g, const void* b, void* y, int y_type,
+                         int64_t ldy, float* mean, float* rstd, int T, int d, float eps, cudaStream_t st) {
+  if (T <= 0) return MT_OK;
+  if (x_type == MT_F32 && y_type == MT_F32) return ln_fwd<float, float>(x, ldx, g, b, y, ldy, mean, rstd, T, d, eps, st);
+  if (x_type == MT_F32) return ln_fwd<float, bf16>(x, ldx, g, b, y, ldy, mean, rstd, T, d, eps, st);
+  if (y_type == MT_F32) return ln_fwd<bf16, float>(x, ldx, g, b, y, ldy, mean, rstd, T, d, eps, st);
+  return ln_fwd<bf16, bf16>(x, ldx, g, b, y, ldy, mean, rstd, T, d, eps, st);
+}
+
+size_t layernorm_bwd_partial_floats(int T, int d) { return (size_t)ln_bwd_blocks(T) * 2 * d; }
+
+int launch_layernorm_bwd(const LayerNormBwd& a, cudaStream_t st) {
+  if (a.T <= 0) {  // sums over no rows
+    if (cudaMemsetAsync(a.dg, 0, sizeof(float) * a.d, st) != cudaSuccess) return MT_ERR_CUDA;
+    if (a.db && cudaMemsetAsync(a.db, 0, sizeof(float) * a.d, st) != cudaSuccess) return MT_ERR_CUDA;
+    return MT_OK;
+  }
+  if (a.x_type == MT_F32 && a.dy_type == MT_F32) return ln_bwd<float, float>(a, st);
+  if (a.x_type == MT_F32) return ln_bwd<float, bf16>(a, st);
+  if (a.dy_type == MT_F32) return ln_bwd<bf16, float>(a, st);
+  return ln_bwd<bf16, bf16>(a, st);
+}
+
+}  // namespace mt

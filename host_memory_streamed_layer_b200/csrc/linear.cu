@@ -1,0 +1,707 @@
+// Matrix products with the elementwise part of a layer in their epilogue
+// (sm_100a, tcgen05): none of the products below leaves an intermediate in
+// memory that the next kernel would read back, and none is rounded before the
+// epilogue has used it.
+//   linear      C  = R + drop(act(A W^T + bias)),  Z = A W^T + bias kept on request
+//   linear_bwd  dZ = drop(dY W) act'(Z),  db_j = sum over rows of dZ_j
+//   gated       h  = act(x Wg^T) (x Wu^T),  [gate | up] kept on request
+//   gated_bwd   dh = dy Wd;  dgate = dh up act'(gate),  dup = dh act(gate),  h = act(gate) up
+//
+// Structure (persistent over output tiles):
+//   warp 0      TMA producer: fills a ring of shared-memory stages
+//   warp 1      MMA issuer: one thread issues tcgen05.mma on 128 x BN x 16
+//               (256 x BN x 16 for a pair of CTAs)
+//   warps 2..   epilogue: tcgen05.ld from tensor memory, elementwise, store
+// The accumulator is double-buffered in tensor memory (2 x BN columns), so the
+// epilogue of one tile runs under the main loop of the next.
+//
+// The gated product is one product whose B tile holds BN / 2 rows of Wg and
+// the same BN / 2 rows of Wu: gate and up of an element land in the same lane
+// of tensor memory, BN / 2 columns apart. In a pair of CTAs the first stages
+// the rows of Wg and the second those of Wu.
+#include "act_dropout.cuh"
+
+namespace mt {
+
+namespace {
+
+constexpr int BM = 128;
+constexpr int BK = 64;       // 64 bf16 = 128 bytes: one swizzle row
+constexpr int GROUP_M = 16;  // tile raster: 16 M-tiles share a band of N-tiles
+
+enum Epi : int { E_LINEAR_BF16, E_LINEAR_F32, E_BWD, E_GATED, E_GATED_BWD };
+
+template <int BN, bool PAIR>
+struct Cfg {
+  static constexpr int TILE_M = PAIR ? 2 * BM : BM;
+  static constexpr int B_ROWS = PAIR ? BN / 2 : BN;  // rows of B that one CTA stages
+  static constexpr int A_BYTES = BM * BK * 2;
+  static constexpr int B_BYTES = B_ROWS * BK * 2;
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+  static constexpr int STAGES = 196608 / STAGE_BYTES < 9 ? 196608 / STAGE_BYTES : 9;  // 192 KB of operands at most
+  static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + 256;
+  static constexpr uint32_t TMEM_COLS = 2 * BN;  // 64, 128, 256 or 512
+  // Two epilogue warps to a lane quarter once the tile is wide enough to share.
+  static constexpr int EPI_WARPS = BN >= 128 ? 8 : 4;
+  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+};
+
+struct Params {
+  int M, N, K;  // N: columns of the output (of each of gate and up)
+  int act;
+  DropDesc drop;
+  const bf16* bias;
+  const void* R;
+  int64_t ldr;
+  bf16* Z;  // linear: written; linear_bwd: read
+  int64_t ldz;
+  void* C;
+  int64_t ldc;
+  bf16* gu;  // gated: written (NULL: not kept); gated_bwd: read
+  int64_t ldgu;
+  bf16* dgu;  // gated_bwd
+  int64_t lddgu;
+  float* part;  // linear_bwd: sums over 32 rows, [ceil(M / 32), N]; NULL: none
+  int* err;
+  uint64_t wait_ns;  // limit of the single-CTA form's main-loop waits; 0: give up at the first incomplete poll
+};
+
+__device__ __forceinline__ void tile_coords(int tile, int num_m, int num_n, int& mb, int& nb) {
+  const int per_group = GROUP_M * num_n;
+  const int g = tile / per_group;
+  const int first_m = g * GROUP_M;
+  const int gsize = min(num_m - first_m, GROUP_M);
+  const int r = tile - g * per_group;
+  mb = first_m + r % gsize;
+  nb = r / gsize;
+}
+
+// Sums of 32 columns over the warp's 32 lanes: lane i receives column i's.
+// Each step halves the columns a lane holds, so 31 exchanges do all 32.
+__device__ __forceinline__ float column_sums32(float (&v)[32], int lane) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) {
+    const bool hi = lane & o;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float keep = hi ? v[i + o] : v[i];
+      const float send = hi ? v[i] : v[i + o];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+  return v[0];
+}
+
+// ---------------------------------------------------------------------------
+// Epilogues of 32 columns of one row. `a` is the accumulator (and `b` the up
+// half of a gated tile); every lane of the warp calls with its own row.
+// ---------------------------------------------------------------------------
+template <int ACT, typename T>
+__device__ __forceinline__ void linear_chunk(const Params& p, const DropKey& key, int row, int col0,
+                                             const uint32_t (&a)[32]) {
+  if (row >= p.M) return;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int c = col0 + 8 * j, n = p.N - c;
+    if (n <= 0) break;
+    float v[8], t[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(a[8 * j + e]);
+    if (p.bias) {
+      load8n(p.bias + c, n, t);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += t[e];
+    }
+    if (p.Z) store8n(p.Z + row * p.ldz + c, n, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = act_value<ACT>(v[e]);
+    if (p.drop.on) {
+      drop4(v, c >> 2, p.drop.row0 + (uint32_t)row, p.drop, key);
+      drop4(v + 4, (c >> 2) + 1, p.drop.row0 + (uint32_t)row, p.drop, key);
+    }
+    if (p.R) {
+      load8n(reinterpret_cast<const T*>(p.R) + row * p.ldr + c, n, t);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] += t[e];
+    }
+    store8n(reinterpret_cast<T*>(p.C) + row * p.ldc + c, n, v);
+  }
+}
+
+template <int ACT>
+__device__ __forceinline__ void bwd_chunk(const Params& p, const DropKey& key, int row, int col0,
+                                          const uint32_t (&a)[32], int lane) {
+  float v[32];
+  const bool ok = row < p.M;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int c = col0 + 8 * j, n = ok ? p.N - c : 0;
+    float(&w)[8] = *reinterpret_cast<float(*)[8]>(&v[8 * j]);
+    if (n <= 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] = 0.f;
+      continue;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = __uint_as_float(a[8 * j + e]);
+    if (ACT != MT_ACT_NONE) {
+      float t[8];
+      load8n(p.Z + row * p.ldz + c, n, t);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) w[e] *= act_slope<ACT>(t[e]);
+    }
+    if (p.drop.on) {  // last, so that a dropped element is 0 whatever Z holds there
+      drop4(w, c >> 2, p.drop.row0 + (uint32_t)row, p.drop, key);
+      drop4(w + 4, (c >> 2) + 1, p.drop.row0 + (uint32_t)row, p.drop, key);
+    }
+    store8n(reinterpret_cast<bf16*>(p.C) + row * p.ldc + c, n, w);
+  }
+  if (p.part) {
+    const float s = column_sums32(v, lane);  // rows and columns outside the matrix hold zeros
+    const int first = row - lane, col = col0 + lane;
+    if (first < p.M && col < p.N) p.part[(int64_t)(first >> 5) * p.N + col] = s;
+  }
+}
+
+template <int ACT>
+__device__ __forceinline__ void gated_chunk(const Params& p, int row, int col0, const uint32_t (&a)[32],
+                                            const uint32_t (&b)[32]) {
+  if (row >= p.M) return;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int c = col0 + 8 * j;
+    if (c >= p.N) break;  // N is a multiple of 8
+    float g[8], u[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      g[e] = __uint_as_float(a[8 * j + e]);
+      u[e] = __uint_as_float(b[8 * j + e]);
+    }
+    if (p.gu) {
+      bf16* o = p.gu + row * p.ldgu + c;
+      store8(o, g);
+      store8(o + p.N, u);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u[e] *= act_value<ACT>(g[e]);
+    store8(reinterpret_cast<bf16*>(p.C) + row * p.ldc + c, u);
+  }
+}
+
+template <int ACT>
+__device__ __forceinline__ void gated_bwd_chunk(const Params& p, int row, int col0, const uint32_t (&a)[32]) {
+  if (row >= p.M) return;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int c = col0 + 8 * j;
+    if (c >= p.N) break;  // N is a multiple of 8
+    float g[8], u[8], h[8];
+    const bf16* in = p.gu + row * p.ldgu + c;
+    load8(in, g);
+    load8(in + p.N, u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float dh = __uint_as_float(a[8 * j + e]);
+      float value, slope;
+      act_both<ACT>(g[e], value, slope);
+      h[e] = value * u[e];
+      g[e] = dh * u[e] * slope;
+      u[e] = dh * value;
+    }
+    bf16* o = p.dgu + row * p.lddgu + c;
+    store8(o, g);
+    store8(o + p.N, u);
+    if (p.C) store8(reinterpret_cast<bf16*>(p.C) + row * p.ldc + c, h);
+  }
+}
+
+// One epilogue warp's share of a tile: OW output columns of 32 rows.
+template <int EPI, int BN, int OW>
+__device__ __forceinline__ void epilogue(const Params& p, const DropKey& key, uint32_t tbase, int row, int col_base,
+                                         int lane) {
+#pragma unroll 1
+  for (int c = 0; c < OW; c += 32) {
+    const int col0 = col_base + c;
+    if (col0 >= p.N) break;
+    uint32_t a[32];
+    tmem_ld_32x32b_x32(tbase + c, a);
+    if (EPI == E_GATED) {
+      uint32_t b[32];
+      tmem_ld_32x32b_x32(tbase + BN / 2 + c, b);
+      tmem_ld_wait();
+      MT_WITH_ACT(p.act, (gated_chunk<ACT>(p, row, col0, a, b)));
+      continue;
+    }
+    tmem_ld_wait();
+    if (EPI == E_LINEAR_BF16) {
+      MT_WITH_ACT(p.act, (linear_chunk<ACT, bf16>(p, key, row, col0, a)));
+    } else if (EPI == E_LINEAR_F32) {
+      MT_WITH_ACT(p.act, (linear_chunk<ACT, float>(p, key, row, col0, a)));
+    } else if (EPI == E_BWD) {
+      MT_WITH_ACT(p.act, (bwd_chunk<ACT>(p, key, row, col0, a, lane)));
+    } else if (EPI == E_GATED_BWD) {
+      MT_WITH_ACT(p.act, (gated_bwd_chunk<ACT>(p, row, col0, a)));
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The kernel. PAIR: a cluster of two CTAs computes 256 rows with
+// tcgen05.mma.cta_group::2; each stages its own 128 rows of A and half of B's
+// rows, the leader (rank 0) issues the MMAs, both CTAs' copies complete on the
+// leader's `full` barriers, the leader's commits release both CTAs' `empty`
+// stages and both `tfull` accumulators, and both CTAs' epilogue warps release
+// the leader's `tempty`. B_MN: B is stored [K, N]. tmB2 is Wu's map for a
+// gated product and unused otherwise.
+// ---------------------------------------------------------------------------
+template <int BN, bool PAIR, bool B_MN, int EPI>
+__global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
+    k_linear(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+             const __grid_constant__ CUtensorMap tmB2, const __grid_constant__ Params p) {
+  using C = Cfg<BN, PAIR>;
+  constexpr bool GATED = EPI == E_GATED;
+  constexpr int ON = GATED ? BN / 2 : BN;  // output columns of a tile
+  static_assert(!B_MN || BN >= 64, "an MN-major operand is staged 64 columns at a time");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE_BYTES);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* tfull = empty + C::STAGES;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0;
+  const uint64_t limit = PAIR ? kWaitLimitNs : p.wait_ns;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], C::EPI_WARPS * (PAIR ? 2 : 1));
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    if (GATED) tma_prefetch_desc(&tmB2);
+  }
+  if (warp == 1) {
+    if (PAIR) {
+      tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(tmem_slot, C::TMEM_COLS);
+      tmem_relinquish();
+    }
+  }
+  tc_fence_before();
+  if (PAIR)
+    cluster_sync();  // barrier initialisation and the allocation are visible to both CTAs
+  else
+    __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+
+  const int num_m = (p.M + C::TILE_M - 1) / C::TILE_M;
+  const int num_n = (p.N + ON - 1) / ON;
+  const int num_tiles = num_m * num_n;
+  const int num_kb = (p.K + BK - 1) / BK;
+  const int first_tile = PAIR ? blockIdx.x >> 1 : blockIdx.x;
+  const int tile_step = PAIR ? gridDim.x >> 1 : gridDim.x;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- TMA producer ----------------
+      int stage = 0;
+      uint32_t phase = 0;
+      int issued = 0;  // stages filled so far (for the teardown)
+      const uint32_t fb0 = PAIR ? mapa_shared(smem_u32(&full[0]), 0) : 0;  // the leader's full barriers
+      bool ok = true;
+      for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
+        int mb, nb;
+        tile_coords(tile, num_m, num_n, mb, nb);
+        const int m0 = mb * C::TILE_M + (int)rank * BM;
+        // A pair's B rows are split over its CTAs; a gated tile has one half from each weight.
+        const int n0 = nb * ON + (PAIR && !GATED ? (int)rank * (BN / 2) : 0);
+        const CUtensorMap* mB = PAIR && GATED && rank ? &tmB2 : &tmB;
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (*abort_flag || !mbar_wait(&empty[stage], phase ^ 1, limit)) {
+            record_error(p.err, DEV_TIMEOUT_PRODUCER);
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+          uint8_t* sa = smem + stage * C::STAGE_BYTES;
+          uint8_t* sb = sa + C::A_BYTES;
+          const int k0 = kb * BK;
+          if (PAIR) {
+            const uint32_t fb = fb0 + 8 * stage;
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::STAGE_BYTES);
+            tma_load_2d_pair(sa, &tmA, fb, k0, m0);
+            if (!B_MN) {
+              tma_load_2d_pair(sb, mB, fb, k0, n0);
+            } else {
+#pragma unroll
+              for (int i = 0; i < C::B_ROWS / 64; ++i) tma_load_2d_pair(sb + i * 8192, mB, fb, n0 + i * 64, k0);
+            }
+          } else {
+            mbar_arrive_expect_tx(&full[stage], C::STAGE_BYTES);
+            tma_load_2d(sa, &tmA, &full[stage], k0, m0);
+            if (GATED) {
+              tma_load_2d(sb, &tmB, &full[stage], k0, n0);
+              tma_load_2d(sb + C::B_BYTES / 2, &tmB2, &full[stage], k0, n0);
+            } else if (!B_MN) {
+              tma_load_2d(sb, &tmB, &full[stage], k0, n0);
+            } else {
+#pragma unroll
+              for (int i = 0; i < C::B_ROWS / 64; ++i) tma_load_2d(sb + i * 8192, &tmB, &full[stage], n0 + i * 64, k0);
+            }
+          }
+          ++issued;
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (ok) {
+        // Wait until the MMA has released every stage, so that no commit is on
+        // its way to this CTA's barriers when it exits. If another role gives
+        // up meanwhile, the MMA may never release them: drain the copies below.
+        for (int i = 0; i < C::STAGES && ok; ++i) {
+          const uint64_t t0 = globaltimer();
+          while (!mbar_wait(&empty[stage], phase ^ 1, 0)) {
+            if (!PAIR && *abort_flag) {
+              ok = false;
+              break;
+            }
+            if (globaltimer() - t0 > kWaitLimitNs) {
+              record_error(p.err, DEV_TIMEOUT_TEARDOWN);
+              *abort_flag = 1;
+              ok = false;
+              break;
+            }
+          }
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (!ok && rank == 0) {
+        // Every issued copy lands before the shared memory goes away: stage s
+        // was last filled by fill s + STAGES q (the largest below `issued`), in
+        // phase q mod 2. The leader's barriers count both CTAs' bytes.
+        for (int s = 0; s < C::STAGES && s < issued; ++s) {
+          const int q = (issued - 1 - s) / C::STAGES;
+          if (!mbar_wait(&full[s], (uint32_t)(q & 1))) record_error(p.err, DEV_TIMEOUT_TEARDOWN);
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // ---------------- MMA issuer ----------------
+      constexpr uint32_t idesc = idesc_bf16_f32(C::TILE_M, BN, false, B_MN);
+      // Descriptors of stage 0; stages and k-steps only move the start address.
+      const uint32_t s0 = smem_u32(smem);
+      const uint64_t a0 = sdesc_sw128(s0, 16, 1024);
+      const uint64_t b0 = sdesc_sw128(s0 + C::A_BYTES, B_MN ? 8192 : 16, 1024);
+      constexpr uint32_t kStage = C::STAGE_BYTES >> 4;
+      constexpr uint32_t kAStep = 32 >> 4, kBStep = (B_MN ? 2048 : 32) >> 4;
+      const uint32_t full0 = smem_u32(&full[0]), empty0 = smem_u32(&empty[0]);
+      const uint32_t empty0_peer = PAIR ? mapa_shared(empty0, 1) : 0;
+      int stage = 0;
+      uint32_t phase = 0;
+      int acc = 0;
+      uint32_t acc_phase = 0;
+      bool ok = true;
+      bool issued = false;
+      for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
+        const bool free_acc = PAIR ? mbar_wait_cluster(&tempty[acc], acc_phase ^ 1)
+                                   : mbar_wait(&tempty[acc], acc_phase ^ 1, limit);
+        if (*abort_flag || !free_acc) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * BN;
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (!mbar_wait_u32(full0 + 8 * stage, phase, limit)) {
+            ok = false;
+            break;
+          }
+          // The stage's bytes were written by TMA and published through this
+          // mbarrier, which orders them for the MMAs' reads: no tcgen05 fence.
+          const uint64_t ad = a0 + stage * kStage, bd = b0 + stage * kStage;
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            if (PAIR)
+              umma_bf16_pair(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, (kb | kk) != 0);
+            else
+              umma_bf16(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, (kb | kk) != 0);
+          }
+          issued = true;
+          if (PAIR) {
+            umma_commit_pair(empty0 + 8 * stage);
+            umma_commit_pair(empty0_peer + 8 * stage);
+          } else {
+            umma_commit_u32(empty0 + 8 * stage);
+          }
+          if (++stage == C::STAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        if (PAIR) {
+          const uint32_t tb = smem_u32(&tfull[acc]);
+          umma_commit_pair(tb);
+          umma_commit_pair(mapa_shared(tb, 1));
+        } else {
+          umma_commit(&tfull[acc]);
+        }
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1;
+        }
+      }
+      if (!ok) {
+        record_error(p.err, DEV_TIMEOUT_MMA);
+        *abort_flag = 1;
+      }
+      // Every MMA issued here completes before tensor memory is freed, also
+      // when the epilogue gave up on an accumulator it will never read.
+      if (issued) {
+        if (PAIR)
+          umma_commit_pair(smem_u32(drain));
+        else
+          umma_commit(drain);
+        if (!mbar_wait(drain, 0)) record_error(p.err, DEV_TIMEOUT_TEARDOWN);
+      }
+    }
+  } else {
+    // ---------------- epilogue ----------------
+    const int quarter = warp & 3;                 // tensor-memory lanes this warp may read
+    constexpr int OW = ON / (C::EPI_WARPS / 4);   // output columns of this warp's share
+    const int share = ((warp - 2) >> 2) * OW;
+    const DropKey key = drop_key(p.drop);
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int tile = first_tile; tile < num_tiles; tile += tile_step) {
+      // warp-uniform outcome: the tcgen05.ld below is warp-collective
+      if (__any_sync(0xffffffffu, *abort_flag) ||
+          !__all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, limit))) {
+        record_error(p.err, DEV_TIMEOUT_EPILOGUE);
+        *abort_flag = 1;
+        break;
+      }
+      tc_fence_after();
+      int mb, nb;
+      tile_coords(tile, num_m, num_n, mb, nb);
+      const int row = mb * C::TILE_M + (int)rank * BM + quarter * 32 + lane;
+      const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * BN + share;
+      epilogue<EPI, BN, OW>(p, key, tbase, row, nb * ON + share, lane);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR && rank)
+          mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
+        else
+          mbar_arrive(&tempty[acc]);
+      }
+      if (++acc == 2) {
+        acc = 0;
+        acc_phase ^= 1;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncwarp();
+  if (PAIR)
+    cluster_sync();  // no MMA of the pair and no tensor-memory read is outstanding
+  else
+    __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    if (PAIR)
+      tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+    else
+      tmem_dealloc(tmem_base, C::TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+// ---------------------------------------------------------------------------
+constexpr int kMaxDevices = 64;
+
+// What a launch needs: operands and the tile-independent parameters.
+struct Op {
+  const void* A;
+  int64_t lda;
+  const void* B;
+  const void* B2;  // Wu of a gated product
+  int64_t ldb;
+  Params p;
+};
+
+template <int BN, bool PAIR, bool B_MN, int EPI>
+int launch(const Op& o, int device, int num_sms, cudaStream_t st) {
+  using C = Cfg<BN, PAIR>;
+  constexpr bool GATED = EPI == E_GATED;
+  constexpr int ON = GATED ? BN / 2 : BN;
+  auto kernel = k_linear<BN, PAIR, B_MN, EPI>;
+  const Params& p = o.p;
+  CUtensorMap ta, tb, tb2;
+  bool ok = make_tensor_map_2d_bf16(&ta, o.A, p.K, p.M, o.lda, BM);
+  const int b_box = GATED && !PAIR ? C::B_ROWS / 2 : C::B_ROWS;
+  ok = ok && (B_MN ? make_tensor_map_2d_bf16(&tb, o.B, p.N, p.K, o.ldb, 64)
+                   : make_tensor_map_2d_bf16(&tb, o.B, p.K, p.N, o.ldb, b_box));
+  tb2 = tb;
+  if (GATED) ok = ok && make_tensor_map_2d_bf16(&tb2, o.B2, p.K, p.N, o.ldb, b_box);
+  if (!ok) return MT_ERR_ARG;
+
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(C::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  if (PAIR) {
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  // Per device, once: the shared-memory limit and the CTAs (pairs) that can be
+  // resident together. Threads that race here write the same value.
+  static int resident[kMaxDevices] = {};
+  if (resident[device] == 0) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+      return MT_ERR_CUDA;
+    int r = PAIR ? num_sms / 2 : num_sms;
+    if (PAIR) {
+      int n = 0;
+      cfg.gridDim = dim3(2 * r, 1, 1);
+      if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0)
+        r = n < r ? n : r;
+      else
+        cudaGetLastError();
+    }
+    resident[device] = r;
+  }
+  const int64_t tiles = (int64_t)((p.M + C::TILE_M - 1) / C::TILE_M) * ((p.N + ON - 1) / ON);
+  if (tiles > INT32_MAX / 2) return MT_ERR_ARG;
+  const int n = tiles < resident[device] ? (int)tiles : resident[device];
+  cfg.gridDim = dim3(PAIR ? 2 * n : n, 1, 1);
+  cudaLaunchKernelEx(&cfg, kernel, ta, tb, tb2, p);
+  return launch_status();
+}
+
+// Tiles dealt to `n` resident CTAs or pairs, in whole waves.
+int64_t waves(int64_t M, int64_t N, int tm, int tn, int n) {
+  const int64_t tiles = ((M + tm - 1) / tm) * ((N + tn - 1) / tn);
+  return (tiles + n - 1) / n;
+}
+
+// The tile is the one whose waves cost least, where a k-block of a 128 x BN
+// tile is taken to cost BN + 32 (its columns on the tensor core, and a fixed
+// part for staging A and for the waits) and a pair's 256-row tile to cost as
+// much as one CTA's 128 rows.
+template <bool B_MN, int EPI>
+int dispatch(const Op& o, cudaStream_t st) {
+  int device = 0, sms = 0;
+  if (cudaGetDevice(&device) != cudaSuccess || device >= kMaxDevices) return MT_ERR_CUDA;
+  static int num_sms[kMaxDevices] = {};
+  if (num_sms[device] == 0) {
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || sms <= 0)
+      return MT_ERR_CUDA;
+    num_sms[device] = sms;
+  }
+  sms = num_sms[device];
+  constexpr int G = EPI == E_GATED ? 2 : 1;  // a gated tile spends half of its columns on each of gate and up
+  const int family = gemm_variant_now();
+  int best = 0;
+  int64_t cost = INT64_MAX;
+  auto consider = [&](int id, int bn, bool pair) {
+    const int64_t w = waves(o.p.M, o.p.N, pair ? 2 * BM : BM, bn / G, pair ? sms / 2 : sms);
+    const int64_t c = w * (bn + 32);
+    if (c < cost) cost = c, best = id;
+  };
+  if (family != 1) consider(0, 256, true);
+  if (family != 1) consider(1, 128, true);
+  if (family != 2) {
+    consider(2, 256, false);
+    consider(3, 128, false);
+    consider(4, 64, false);
+    if (!B_MN && G == 1) consider(5, 32, false);
+  }
+  switch (best) {
+    case 0: return launch<256, true, B_MN, EPI>(o, device, sms, st);
+    case 1: return launch<128, true, B_MN, EPI>(o, device, sms, st);
+    case 2: return launch<256, false, B_MN, EPI>(o, device, sms, st);
+    case 3: return launch<128, false, B_MN, EPI>(o, device, sms, st);
+    case 4: return launch<64, false, B_MN, EPI>(o, device, sms, st);
+    default:
+      if constexpr (!B_MN && G == 1) return launch<32, false, B_MN, EPI>(o, device, sms, st);
+      return MT_ERR_ARG;
+  }
+}
+
+}  // namespace
+
+int launch_linear_fwd(const LinearFwd& a, const DropDesc& drop, cudaStream_t st, int* dev_err) {
+  Op o{};
+  o.A = a.A, o.lda = a.lda, o.B = a.W, o.ldb = a.ldw;
+  Params& p = o.p;
+  p.M = a.M, p.N = a.N, p.K = a.K, p.act = a.act, p.drop = drop;
+  p.bias = (const bf16*)a.bias, p.R = a.R, p.ldr = a.ldr, p.Z = (bf16*)a.Z, p.ldz = a.ldz, p.C = a.C, p.ldc = a.ldc;
+  p.err = dev_err, p.wait_ns = gemm_wait_limit_now();
+  return a.out_type == MT_F32 ? dispatch<false, E_LINEAR_F32>(o, st) : dispatch<false, E_LINEAR_BF16>(o, st);
+}
+
+size_t linear_bwd_partial_floats(int M, int N) { return (size_t)((M + 31) / 32) * N; }
+
+int launch_linear_bwd_act(const LinearBwd& a, const DropDesc& drop, cudaStream_t st, int* dev_err) {
+  Op o{};
+  o.A = a.dY, o.lda = a.lddy, o.B = a.W, o.ldb = a.ldw;
+  Params& p = o.p;
+  p.M = a.M, p.N = a.N, p.K = a.K, p.act = a.act, p.drop = drop;
+  p.Z = (bf16*)a.Z, p.ldz = a.ldz, p.C = a.dZ, p.ldc = a.lddz, p.part = a.db ? a.part : nullptr;
+  p.err = dev_err, p.wait_ns = gemm_wait_limit_now();
+  if (const int rc = dispatch<true, E_BWD>(o, st)) return rc;
+  return a.db ? launch_column_sums(a.part, (a.M + 31) / 32, a.N, a.N, a.db, a.N, nullptr, st) : MT_OK;
+}
+
+int launch_gated_ffn_fwd(const void* x, int64_t ldx, const void* Wgu, int64_t ldw, int act, void* gu, int64_t ldgu,
+                         void* h, int64_t ldh, int M, int F, int K, cudaStream_t st, int* dev_err) {
+  Op o{};
+  o.A = x, o.lda = ldx, o.B = Wgu, o.B2 = (const bf16*)Wgu + (int64_t)F * ldw, o.ldb = ldw;
+  Params& p = o.p;
+  p.M = M, p.N = F, p.K = K, p.act = act, p.gu = (bf16*)gu, p.ldgu = ldgu, p.C = h, p.ldc = ldh;
+  p.err = dev_err, p.wait_ns = gemm_wait_limit_now();
+  return dispatch<false, E_GATED>(o, st);
+}
+
+int launch_gated_ffn_bwd(const void* dy, int64_t lddy, const void* Wd, int64_t ldw, const void* gu, int64_t ldgu,
+                         int act, void* dgu, int64_t lddgu, void* h, int64_t ldh, int M, int F, int K, cudaStream_t st,
+                         int* dev_err) {
+  Op o{};
+  o.A = dy, o.lda = lddy, o.B = Wd, o.ldb = ldw;
+  Params& p = o.p;
+  p.M = M, p.N = F, p.K = K, p.act = act, p.gu = (bf16*)gu, p.ldgu = ldgu, p.dgu = (bf16*)dgu, p.lddgu = lddgu;
+  p.C = h, p.ldc = ldh, p.err = dev_err, p.wait_ns = gemm_wait_limit_now();
+  return dispatch<true, E_GATED_BWD>(o, st);
+}
+
+}  // namespace mt

@@ -53,6 +53,9 @@ int gemm_variant(int v);
 int attention_fwd_variant(int v);
 // Main-loop wait limit (ns) of later single-CTA GEMM launches; returns the previous one.
 uint64_t gemm_wait_limit_ns(uint64_t ns);
+// The family (MT_GEMM_VARIANT read on first use) and the limit now in force.
+int gemm_variant_now();
+uint64_t gemm_wait_limit_now();
 
 // 2-D bf16 TMA map: inner (contiguous) extent, outer extent, row pitch ld
 // (elements), box {64, box_outer}, 128-byte swizzle, zero fill out of bounds.
@@ -125,6 +128,79 @@ int launch_moe_dy(const float* dy, const float* ye, const int32_t* slot_of, cons
 int launch_moe_router_bwd(const float* gate, const float* dgate, const int32_t* idx, const void* w, const void* Wr,
                           const float* dxe, const int32_t* slot_of, int T, int k, int d, int E, float* dlogits,
                           float* dWr, float* dw, cudaStream_t st);
+
+// Layer norm, dropout and the products with an elementwise epilogue
+// (layernorm.cu, dropout.cu, linear.cu). Types are MT_F32 or MT_BF16; the
+// caller has checked the arguments. DropDesc: act_dropout.cuh.
+struct DropDesc;
+struct LayerNormBwd {
+  const void* x;
+  int x_type;  // of x, dres and dx
+  int64_t ldx;
+  const void* g;
+  const float* mean;
+  const float* rstd;
+  const void* dy;
+  int dy_type;
+  int64_t lddy;
+  const void* dres;  // may be NULL; may be dx
+  int64_t lddres;
+  void* dx;
+  void* dx_bf16;  // may be NULL; pitch lddx
+  int64_t lddx;
+  float* part;
+  float* dg;
+  float* db;  // may be NULL
+  int T, d;
+};
+int launch_layernorm_fwd(const void* x, int x_type, int64_t ldx, const void* g, const void* b, void* y, int y_type,
+                         int64_t ldy, float* mean, float* rstd, int T, int d, float eps, cudaStream_t st);
+size_t layernorm_bwd_partial_floats(int T, int d);
+int launch_layernorm_bwd(const LayerNormBwd& a, cudaStream_t st);
+int launch_dropout(const void* x, int x_type, int64_t ldx, const DropDesc& drop, const void* res, int64_t ldr, void* y,
+                   int y_type, int64_t ldy, int T, int d, cudaStream_t st);
+size_t act_bwd_partial_floats(int M, int N);
+int launch_act_bwd(const void* dc, int dc_type, int64_t lddc, const void* z, int64_t ldz, int act,
+                   const DropDesc& drop, void* dz, int64_t lddz, float* part, float* db, int M, int N,
+                   cudaStream_t st);
+struct LinearFwd {
+  const void* A;
+  int64_t lda;
+  const void* W;
+  int64_t ldw;
+  const void* bias;  // may be NULL
+  int act;
+  const void* R;  // may be NULL; of out_type; may be C
+  int64_t ldr;
+  void* Z;  // may be NULL
+  int64_t ldz;
+  void* C;
+  int out_type;
+  int64_t ldc;
+  int M, N, K;
+};
+int launch_linear_fwd(const LinearFwd& a, const DropDesc& drop, cudaStream_t st, int* dev_err);
+struct LinearBwd {
+  const void* dY;
+  int64_t lddy;
+  const void* W;
+  int64_t ldw;
+  const void* Z;  // may be NULL without an activation; may be dZ
+  int64_t ldz;
+  int act;
+  void* dZ;
+  int64_t lddz;
+  float* part;
+  float* db;  // may be NULL
+  int M, N, K;
+};
+size_t linear_bwd_partial_floats(int M, int N);
+int launch_linear_bwd_act(const LinearBwd& a, const DropDesc& drop, cudaStream_t st, int* dev_err);
+int launch_gated_ffn_fwd(const void* x, int64_t ldx, const void* Wgu, int64_t ldw, int act, void* gu, int64_t ldgu,
+                         void* h, int64_t ldh, int M, int F, int K, cudaStream_t st, int* dev_err);
+int launch_gated_ffn_bwd(const void* dy, int64_t lddy, const void* Wd, int64_t ldw, const void* gu, int64_t ldgu,
+                         int act, void* dgu, int64_t lddgu, void* h, int64_t ldh, int M, int F, int K, cudaStream_t st,
+                         int* dev_err);
 
 int launch_rmsnorm_fwd(const float* x, const void* g, void* y, float* rstd, int T, int d, float eps, cudaStream_t st);
 int rmsnorm_bwd_blocks(int T);

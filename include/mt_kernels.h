@@ -166,6 +166,152 @@ int mt_k_gemm_bf16_rope(const void* A, int64_t lda, const void* B, int64_t ldb, 
                         int K, int rope_cols, int hd, int s, const float* cos_tab, const float* sin_tab, void* stream,
                         int32_t* dev_err);
 
+/* ---------------------------------------------------------------------------
+ * The parts of a decoder block with layer norms, biased linear layers, dropout
+ * and a gated feed-forward part, each with its gradient (families beside the
+ * Llama-style one: saify.me, "Who this is actually for": "The repo supports
+ * many architectures"; gradients written out by hand as in
+ * intelligentliving.co, "Checkpointing, Manual Gradients, and CPU-Side
+ * Optimizer Steps").
+ *
+ * In addition to the conventions above:
+ *   - matrices are row-major with a pitch (ld*) in elements, at least the row's
+ *     width; bases are 16-byte aligned and pitches multiples of 16 bytes, so a
+ *     pitch is a multiple of 4 (fp32) or 8 (bf16) elements. Widths may be odd:
+ *     nothing behind a row's last element is read or written;
+ *   - all sums, statistics and activations are fp32; a bf16 output is rounded
+ *     once, to nearest even, from the fp32 result;
+ *   - the calls are deterministic: the same inputs give the same bits;
+ *   - buffers may not overlap unless a call allows it; scratch belongs to one
+ *     call in flight at a time (calls that may run at once, captured graphs
+ *     included, need scratch of their own);
+ *   - rows, columns and depths up to 2^30;
+ *   - the pointers and the stream belong to the current device.
+ * ------------------------------------------------------------------------- */
+
+/* Element types. */
+#define MT_F32 0
+#define MT_BF16 1
+
+/* Activations: identity; max(z, 0); z Phi(z) with the normal distribution
+ * function; its tanh form z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2;
+ * z / (1 + exp(-z)). */
+#define MT_ACT_NONE 0
+#define MT_ACT_RELU 1
+#define MT_ACT_GELU 2
+#define MT_ACT_GELU_TANH 3
+#define MT_ACT_SILU 4
+
+/* Dropout drop(v): each element is 0 with probability p (rounded to a multiple
+ * of 2^-32) and v / (1 - p) otherwise; a dropped element is 0 even where v is
+ * NaN or infinite. The mask is never stored: element (t, j) of a matrix takes
+ * word j % 4 of the Philox4x32-10 block (Salmon, Moraes, Dror and Shaw,
+ * "Parallel random numbers: as easy as 1, 2, 3") whose counter is
+ * (j / 4, row0 + t, low and high half of the offset) under the key `seed`, and
+ * is dropped where that word is below p 2^32. So the same numbers give the same
+ * mask in every call, forward and backward, whatever the types and pitches,
+ * and a call on some of the rows (row0: the first one's index in the whole
+ * matrix) gives those rows' part of the whole mask. Give each use of dropout
+ * in a step an offset of its own.
+ * The offset is offset + *offset_dev (modulo 2^64; offset_dev: device int64,
+ * 8-byte aligned, read when the kernel runs; NULL: offset alone), so a captured
+ * graph draws new masks at each replay when the program moves *offset_dev.
+ * 0 <= p < 1, 0 <= row0, row0 + rows <= 2^32. */
+typedef struct mt_dropout {
+  float p;
+  int64_t seed;
+  int64_t offset;
+  const int64_t* offset_dev;
+  int64_t row0;
+} mt_dropout;
+
+/* Layer norm of each row: m = mean x, r = 1 / sqrt(mean (x - m)^2 + eps),
+ *   y_j = (x_j - m) r g_j + b_j.
+ * x [T, d] of x_type, y [T, d] of y_type; g, b bf16 [d] (b NULL: no shift);
+ * mean, rstd fp32 [T] (each may be NULL) receive m and r, which the backward
+ * reads. eps >= 0; d <= 8192 (MT_ERR_CONFIG otherwise). */
+int mt_k_layernorm_fwd(const void* x, int x_type, int64_t ldx, const void* g, const void* b, void* y, int y_type,
+                       int64_t ldy, float* mean, float* rstd, int T, int d, float eps, void* stream);
+
+/* Floats of the scratch that mt_k_layernorm_bwd needs; 0 for sizes it refuses. */
+size_t mt_k_layernorm_bwd_partial_floats(int T, int d);
+
+/* Layer norm backward. With xh_j = (x_j - mean) rstd and w_j = dy_j g_j:
+ *   dx_j = dres_j + rstd (w_j - mean_i w_i - xh_j mean_i(w_i xh_i))
+ *   dg_j = sum over rows of dy_j xh_j,  db_j = sum over rows of dy_j.
+ * x, dres (NULL: zero) and dx [T, d] are of x_type, dy [T, d] of dy_type; g
+ * bf16 [d]; mean, rstd fp32 [T]; dx_bf16 (may be NULL, only for fp32 dx; pitch
+ * lddx, which is then a multiple of 8) receives dx rounded to bf16; dg, db fp32
+ * [d] (db may be NULL); part: scratch of mt_k_layernorm_bwd_partial_floats(T,
+ * d) floats. dx may be dres (same pitch). T = 0 gives zero dg and db. */
+int mt_k_layernorm_bwd(const void* x, int x_type, int64_t ldx, const void* g, const float* mean, const float* rstd,
+                       const void* dy, int dy_type, int64_t lddy, const void* dres, int64_t lddres, void* dx,
+                       void* dx_bf16, int64_t lddx, float* part, float* dg, float* db, int T, int d, void* stream);
+
+/* Dropout and residual: y = res + drop(x). x [T, d] of x_type; res (NULL:
+ * zero) and y [T, d] of y_type; drop as above (NULL or p = 0: nothing is
+ * dropped). The gradient of x is the same call on dy with res NULL. y may be
+ * res, and may be x when the types are equal (same pitch). */
+int mt_k_dropout(const void* x, int x_type, int64_t ldx, const mt_dropout* drop, const void* res, int64_t ldr, void* y,
+                 int y_type, int64_t ldy, int T, int d, void* stream);
+
+/* Linear layer: with U = A W^T + bias,
+ *   C = R + drop(act(U)).
+ * A bf16 [M, K]; W bf16 [N, K]; bias bf16 [N] (NULL: none); R (NULL: none) and
+ * C [M, N] of out_type; Z (may be NULL) receives U in bf16 [M, N], which the
+ * backward reads; drop NULL: no dropout. The product is accumulated in fp32
+ * and U enters act unrounded. K >= 1. C may be R (same pitch). dev_err as for
+ * mt_k_gemm_bf16. */
+int mt_k_linear_fwd(const void* A, int64_t lda, const void* W, int64_t ldw, const void* bias, int act,
+                    const mt_dropout* drop, const void* R, int64_t ldr, void* Z, int64_t ldz, void* C, int out_type,
+                    int64_t ldc, int M, int N, int K, void* stream, int32_t* dev_err);
+
+/* Floats of the scratch that mt_k_linear_bwd_act needs for db; 0 for sizes it refuses. */
+size_t mt_k_linear_bwd_act_partial_floats(int M, int N);
+
+/* Back from a layer's output gradient to the pre-activation of the layer
+ * before it, C = drop(act(Z)) being the input of Y = C W^T:
+ *   dZ = drop(dY W) act'(Z),  db_j = sum over rows of dZ_j (unrounded).
+ * dY bf16 [M, K]; W bf16 [K, N] (the later layer's weight as its forward holds
+ * it); Z, dZ bf16 [M, N] (Z may be NULL with MT_ACT_NONE; dZ may be Z, same
+ * pitch); db fp32 [N] (may be NULL, then part may be too); drop as in the
+ * forward of C. M = 0 gives zero db. The layer's other gradients are products
+ * of mt_k_gemm_bf16: dA = dZ W1, dW1 = dZ^T A. */
+int mt_k_linear_bwd_act(const void* dY, int64_t lddy, const void* W, int64_t ldw, const void* Z, int64_t ldz, int act,
+                        const mt_dropout* drop, void* dZ, int64_t lddz, float* part, float* db, int M, int N, int K,
+                        void* stream, int32_t* dev_err);
+
+/* Floats of the scratch that mt_k_act_bwd needs for db; 0 for sizes it refuses. */
+size_t mt_k_act_bwd_partial_floats(int M, int N);
+
+/* The same step from the gradient dC of C = drop(act(Z)) itself (the last
+ * layer of a block, whose output goes to the residual stream):
+ *   dZ = drop(dC) act'(Z),  db_j = sum over rows of dZ_j (unrounded).
+ * dC [M, N] of dc_type; Z, dZ bf16 [M, N] (Z may be NULL with MT_ACT_NONE; dZ
+ * may be Z, or a bf16 dC, same pitch); db, part as above. */
+int mt_k_act_bwd(const void* dC, int dc_type, int64_t lddc, const void* Z, int64_t ldz, int act,
+                 const mt_dropout* drop, void* dZ, int64_t lddz, float* part, float* db, int M, int N, void* stream);
+
+/* Gated feed-forward part up to its down projection, both projections, the
+ * activation and the product in one kernel:
+ *   gate = x Wg^T, up = x Wu^T, h = act(gate) up.
+ * x bf16 [M, K]; Wgu bf16 [2F, K], Wg's rows before Wu's; h bf16 [M, F]; gu
+ * (may be NULL) receives [gate | up] in bf16 [M, 2F], which the backward
+ * reads. h is computed from the unrounded gate and up (mt_k_gemm_bf16 followed
+ * by mt_k_swiglu_fwd rounds them to bf16 in between). F a multiple of 8,
+ * K >= 1. The output is y = h Wd^T: mt_k_gemm_bf16, or mt_k_linear_fwd. */
+int mt_k_gated_ffn_fwd(const void* x, int64_t ldx, const void* Wgu, int64_t ldw, int act, void* gu, int64_t ldgu,
+                       void* h, int64_t ldh, int M, int F, int K, void* stream, int32_t* dev_err);
+
+/* Its backward from dy, with dh = dy Wd never stored:
+ *   dgate = dh up act'(gate), dup = dh act(gate), h = act(gate) up again.
+ * dy bf16 [M, K]; Wd bf16 [K, F]; gu, dgu bf16 [M, 2F] ([gate | up]; dgu may be
+ * gu, same pitch); h (may be NULL) bf16 [M, F]. The other gradients are
+ * products of mt_k_gemm_bf16: dx = dgu Wgu, dWgu = dgu^T x, dWd = dy^T h. */
+int mt_k_gated_ffn_bwd(const void* dy, int64_t lddy, const void* Wd, int64_t ldw, const void* gu, int64_t ldgu, int act,
+                       void* dgu, int64_t lddgu, void* h, int64_t ldh, int M, int F, int K, void* stream,
+                       int32_t* dev_err);
+
 /* Codes a kernel writes into dev_err when one of its bounded waits runs out
  * (the first code recorded wins). */
 #define MT_DEV_TIMEOUT_PRODUCER 1 /* the copy producer waited too long for a free stage */
