@@ -72,27 +72,35 @@ __device__ __forceinline__ void store8n(T* p, int n, const float (&v)[8]) {
 // (1 + tanh u) / 2 = 1 / (1 + exp(-2u)), which keeps its lower tail exact.
 // ReLU passes NaN on; its slope at 0 is 0.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float logistic(float z) { return 1.f / (1.f + __expf(-z)); }
+__device__ __forceinline__ float logistic(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 
-template <int ACT>
-__device__ __forceinline__ float act_value(float z) {
-  if (ACT == MT_ACT_RELU) return z < 0.f ? 0.f : z;
-  if (ACT == MT_ACT_GELU) return 0.5f * z * (1.f + erff(z * 0.70710678f));
-  if (ACT == MT_ACT_GELU_TANH) return z * logistic(z * (1.59576912f + 0.07135482f * z * z));
-  if (ACT == MT_ACT_SILU) return z * logistic(z);
-  return z;
+// The normal distribution function and exp(-z^2 / 2), which its density and
+// its own approximation share: with x = |z| / sqrt 2 and t = 1 / (1 + p x),
+// erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2) to 1.5e-7 (Abramowitz and Stegun,
+// Handbook of Mathematical Functions, 7.1.26). The lower tail is taken from
+// erfc itself, so nothing cancels there.
+__device__ __forceinline__ float normal_cdf(float z, float& gauss) {
+  const float x = fabsf(z) * 0.70710678f;
+  const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
+  gauss = __expf(-x * x);
+  const float poly =
+      t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
+  const float q = 0.5f * poly * gauss;
+  return z < 0.f ? q : 1.f - q;
 }
 
-// Value and slope together (they share the transcendental).
+// Value and slope together (they share the transcendentals; what a caller does
+// not use is not computed).
 template <int ACT>
 __device__ __forceinline__ void act_both(float z, float& value, float& slope) {
   if (ACT == MT_ACT_RELU) {
     value = z < 0.f ? 0.f : z;
     slope = z > 0.f ? 1.f : 0.f;
   } else if (ACT == MT_ACT_GELU) {
-    const float c = 0.5f * (1.f + erff(z * 0.70710678f));
+    float gauss;
+    const float c = normal_cdf(z, gauss);
     value = z * c;
-    slope = c + z * __expf(-0.5f * z * z) * 0.39894228f;
+    slope = c + z * gauss * 0.39894228f;
   } else if (ACT == MT_ACT_GELU_TANH) {
     const float s = logistic(z * (1.59576912f + 0.07135482f * z * z));
     const float w = s * (1.f - s);  // 0 where s has saturated; the polynomial beside it may then be infinite
@@ -106,6 +114,12 @@ __device__ __forceinline__ void act_both(float z, float& value, float& slope) {
     value = z;
     slope = 1.f;
   }
+}
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+  float v, s;
+  act_both<ACT>(z, v, s);
+  return v;
 }
 template <int ACT>
 __device__ __forceinline__ float act_slope(float z) {

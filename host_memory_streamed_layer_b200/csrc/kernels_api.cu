@@ -259,7 +259,7 @@ extern "C" int mt_k_linear_bwd_act(const void* dY, int64_t lddy, const void* W, 
   if (N == 0) return MT_OK;
   if (M == 0) return !db || cudaMemsetAsync(db, 0, sizeof(float) * N, S(stream)) == cudaSuccess ? MT_OK : MT_ERR_CUDA;
   if (K == 0 || !mat_ok(dY, MT_BF16, lddy, K) || !mat_ok(W, MT_BF16, ldw, N) || !opt_mat_ok(Z, MT_BF16, ldz, N) ||
-      !mat_ok(dZ, MT_BF16, lddz, N) || (act != MT_ACT_NONE && !Z) || (db && !part))
+      !mat_ok(dZ, MT_BF16, lddz, N) || (act != MT_ACT_NONE && !Z) || (db && !part) || !al16(part))
     return MT_ERR_ARG;
   const mt::LinearBwd a{dY, lddy, W, ldw, Z, ldz, act, dZ, lddz, part, db, M, N, K};
   return mt::launch_linear_bwd_act(a, dd, S(stream), dev_err);

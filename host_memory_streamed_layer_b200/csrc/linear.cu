@@ -29,6 +29,9 @@ constexpr int BM = 128;
 constexpr int BK = 64;       // 64 bf16 = 128 bytes: one swizzle row
 constexpr int GROUP_M = 16;  // tile raster: 16 M-tiles share a band of N-tiles
 
+// Each epilogue warp's shared memory: 32 rows x 32 columns of fp32.
+constexpr int EPI_BYTES = 4096;
+
 enum Epi : int { E_LINEAR_BF16, E_LINEAR_F32, E_BWD, E_GATED, E_GATED_BWD };
 
 template <int BN, bool PAIR>
@@ -39,11 +42,11 @@ struct Cfg {
   static constexpr int B_BYTES = B_ROWS * BK * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int STAGES = 196608 / STAGE_BYTES < 9 ? 196608 / STAGE_BYTES : 9;  // 192 KB of operands at most
-  static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + 256;
-  static constexpr uint32_t TMEM_COLS = 2 * BN;  // 64, 128, 256 or 512
   // Two epilogue warps to a lane quarter once the tile is wide enough to share.
   static constexpr int EPI_WARPS = BN >= 128 ? 8 : 4;
   static constexpr int THREADS = 64 + 32 * EPI_WARPS;
+  static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + 256 + EPI_WARPS * EPI_BYTES;
+  static constexpr uint32_t TMEM_COLS = 2 * BN;  // 64, 128, 256 or 512
 };
 
 struct Params {
@@ -61,7 +64,7 @@ struct Params {
   int64_t ldgu;
   bf16* dgu;  // gated_bwd
   int64_t lddgu;
-  float* part;  // linear_bwd: sums over 32 rows, [ceil(M / 32), N]; NULL: none
+  float* part;  // linear_bwd: sums over 32 rows, [ceil(M / 32), N rounded up to 4]; NULL: none
   int* err;
   uint64_t wait_ns;  // limit of the single-CTA form's main-loop waits; 0: give up at the first incomplete poll
 };
@@ -76,172 +79,267 @@ __device__ __forceinline__ void tile_coords(int tile, int num_m, int num_n, int&
   nb = r / gsize;
 }
 
-// Sums of 32 columns over the warp's 32 lanes: lane i receives column i's.
-// Each step halves the columns a lane holds, so 31 exchanges do all 32.
-__device__ __forceinline__ float column_sums32(float (&v)[32], int lane) {
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
-    const bool hi = lane & o;
-#pragma unroll
-    for (int i = 0; i < o; ++i) {
-      const float keep = hi ? v[i + o] : v[i];
-      const float send = hi ? v[i] : v[i + o];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-    }
-  }
-  return v[0];
-}
+// ---------------------------------------------------------------------------
+// Epilogues, one warp on 32 rows x 32 columns at a time. tcgen05.ld gives a
+// lane a whole row; storing from there would touch 32 lines with each
+// instruction. So the block goes through shared memory, and each lane handles
+// 8 columns of the rows lane / 4 + 8 i: 64 bytes of a bf16 row (128 of an fp32
+// one) to four neighbouring lanes.
+// ---------------------------------------------------------------------------
 
-// ---------------------------------------------------------------------------
-// Epilogues of 32 columns of one row. `a` is the accumulator (and `b` the up
-// half of a gated tile); every lane of the warp calls with its own row.
-// ---------------------------------------------------------------------------
-template <int ACT, typename T>
-__device__ __forceinline__ void linear_chunk(const Params& p, const DropKey& key, int row, int col0,
-                                             const uint32_t (&a)[32]) {
-  if (row >= p.M) return;
+// 16-byte unit u of row r of an fp32 block is kept at u ^ (r % 8), so that
+// neither the row-wise writes nor the reads below meet in a bank.
+__device__ __forceinline__ void stage_f32(float* st, int lane, const uint32_t (&a)[32]) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int c = col0 + 8 * j, n = p.N - c;
-    if (n <= 0) break;
-    float v[8], t[8];
+  for (int u = 0; u < 8; ++u)
+    reinterpret_cast<uint4*>(st)[lane * 8 + (u ^ (lane & 7))] =
+        make_uint4(a[4 * u], a[4 * u + 1], a[4 * u + 2], a[4 * u + 3]);
+}
+__device__ __forceinline__ void staged_f32(const float* st, int r, int c8, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(st)[r * 8 + ((2 * c8) ^ (r & 7))];
+  const float4 b = reinterpret_cast<const float4*>(st)[r * 8 + ((2 * c8 + 1) ^ (r & 7))];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+// The same for a block of bf16, 64 bytes to a row: unit u at u ^ (r / 2 % 4).
+__device__ __forceinline__ void stage_bf16(uint4* st, int lane, const float (&v)[32]) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(a[8 * j + e]);
-    if (p.bias) {
-      load8n(p.bias + c, n, t);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += t[e];
-    }
-    if (p.Z) store8n(p.Z + row * p.ldz + c, n, v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = act_value<ACT>(v[e]);
-    if (p.drop.on) {
-      drop4(v, c >> 2, p.drop.row0 + (uint32_t)row, p.drop, key);
-      drop4(v + 4, (c >> 2) + 1, p.drop.row0 + (uint32_t)row, p.drop, key);
-    }
-    if (p.R) {
-      load8n(reinterpret_cast<const T*>(p.R) + row * p.ldr + c, n, t);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] += t[e];
-    }
-    store8n(reinterpret_cast<T*>(p.C) + row * p.ldc + c, n, v);
+  for (int u = 0; u < 4; ++u) {
+    const float w[8] = {v[8 * u],     v[8 * u + 1], v[8 * u + 2], v[8 * u + 3],
+                        v[8 * u + 4], v[8 * u + 5], v[8 * u + 6], v[8 * u + 7]};
+    st[lane * 4 + (u ^ ((lane >> 1) & 3))] = pack8(w);
   }
 }
+__device__ __forceinline__ uint4 staged_bf16(const uint4* st, int r, int u) { return st[r * 4 + (u ^ ((r >> 1) & 3))]; }
 
-template <int ACT>
-__device__ __forceinline__ void bwd_chunk(const Params& p, const DropKey& key, int row, int col0,
-                                          const uint32_t (&a)[32], int lane) {
-  float v[32];
-  const bool ok = row < p.M;
+// What a lane reads beside the accumulator, for its four rows: R (two halves
+// of an fp32 R), Z, or gate and up. It is loaded one block ahead.
+struct Aux {
+  uint4 x[4], y[4];
+};
+
+// Eight bf16 of which n exist, as they are stored; zeros behind them.
+__device__ __forceinline__ uint4 load8_raw(const bf16* p, int n) {
+  if (n >= 8) return *reinterpret_cast<const uint4*>(p);
+  float t[8];
+  load8n(p, n, t);
+  return pack8(t);
+}
+
+// FULL: the block lies inside the matrix, so that nothing is tested per element
+// and the four rows' instructions interleave.
+template <int EPI, bool FULL>
+__device__ __forceinline__ void load_aux(const Params& p, int row0, int col, Aux& a) {
+  const int n = FULL ? 8 : p.N - col;
+  if (!FULL && n <= 0) return;
+  const bool wanted = EPI == E_BWD ? p.act != MT_ACT_NONE : EPI == E_GATED_BWD ? true : p.R != nullptr;
+  if (EPI == E_GATED || !wanted) return;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int c = col0 + 8 * j, n = ok ? p.N - c : 0;
-    float(&w)[8] = *reinterpret_cast<float(*)[8]>(&v[8 * j]);
-    if (n <= 0) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = 0.f;
-      continue;
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = __uint_as_float(a[8 * j + e]);
-    if (ACT != MT_ACT_NONE) {
+  for (int i = 0; i < 4; ++i) {
+    const int row = row0 + 8 * i;
+    if (!FULL && row >= p.M) break;
+    if (EPI == E_LINEAR_BF16) {
+      a.x[i] = load8_raw(reinterpret_cast<const bf16*>(p.R) + row * p.ldr + col, n);
+    } else if (EPI == E_LINEAR_F32) {
       float t[8];
-      load8n(p.Z + row * p.ldz + c, n, t);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] *= act_slope<ACT>(t[e]);
+      load8n(reinterpret_cast<const float*>(p.R) + row * p.ldr + col, n, t);
+      a.x[i] = make_uint4(__float_as_uint(t[0]), __float_as_uint(t[1]), __float_as_uint(t[2]), __float_as_uint(t[3]));
+      a.y[i] = make_uint4(__float_as_uint(t[4]), __float_as_uint(t[5]), __float_as_uint(t[6]), __float_as_uint(t[7]));
+    } else if (EPI == E_BWD) {
+      a.x[i] = load8_raw(p.Z + row * p.ldz + col, n);
+    } else if (EPI == E_GATED_BWD) {
+      const bf16* g = p.gu + row * p.ldgu + col;  // N is a multiple of 8
+      a.x[i] = *reinterpret_cast<const uint4*>(g);
+      a.y[i] = *reinterpret_cast<const uint4*>(g + p.N);
     }
-    if (p.drop.on) {  // last, so that a dropped element is 0 whatever Z holds there
-      drop4(w, c >> 2, p.drop.row0 + (uint32_t)row, p.drop, key);
-      drop4(w + 4, (c >> 2) + 1, p.drop.row0 + (uint32_t)row, p.drop, key);
-    }
-    store8n(reinterpret_cast<bf16*>(p.C) + row * p.ldc + c, n, w);
   }
+}
+template <int EPI>
+__device__ __forceinline__ void load_aux(const Params& p, bool full, int row0, int col, Aux& a) {
+  if (full)
+    load_aux<EPI, true>(p, row0, col, a);
+  else
+    load_aux<EPI, false>(p, row0, col, a);
+}
+
+// The lane's rows of the staged block; rows and columns outside the matrix
+// hold what the product of zeros left there.
+__device__ __forceinline__ void staged_rows(const float* st, int lane, float (&v)[4][8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) staged_f32(st, (lane >> 2) + 8 * i, lane & 3, v[i]);
+}
+__device__ __forceinline__ void drop_rows(const Params& p, const DropKey& key, int row0, int col, float (&v)[4][8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    drop4(v[i], col >> 2, p.drop.row0 + (uint32_t)(row0 + 8 * i), p.drop, key);
+    drop4(v[i] + 4, (col >> 2) + 1, p.drop.row0 + (uint32_t)(row0 + 8 * i), p.drop, key);
+  }
+}
+template <bool FULL, typename T>
+__device__ __forceinline__ void store_rows(T* out, int64_t ld, int row0, int M, int n, const float (&v)[4][8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (FULL || row0 + 8 * i < M) store8n(out + i * 8 * ld, FULL ? 8 : n, v[i]);
+}
+
+template <int ACT, typename T, bool FULL>
+__device__ __forceinline__ void linear_block(const Params& p, const DropKey& key, int row0, int col, int lane,
+                                             const float* st, const Aux& a) {
+  const int n = p.N - col;
+  if (!FULL && n <= 0) return;
+  float v[4][8];
+  staged_rows(st, lane, v);
+  if (p.bias) {
+    float bias[8];
+    load8n(p.bias + col, FULL ? 8 : n, bias);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] += bias[e];
+  }
+  if (p.Z) store_rows<FULL>(p.Z + row0 * p.ldz + col, p.ldz, row0, p.M, n, v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[i][e] = act_value<ACT>(v[i][e]);
+  if (p.drop.on) drop_rows(p, key, row0, col, v);
+  if (p.R) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float t[8];
+      if (sizeof(T) == 2) {
+        unpack8(a.x[i], t);
+      } else {
+        t[0] = __uint_as_float(a.x[i].x), t[1] = __uint_as_float(a.x[i].y);
+        t[2] = __uint_as_float(a.x[i].z), t[3] = __uint_as_float(a.x[i].w);
+        t[4] = __uint_as_float(a.y[i].x), t[5] = __uint_as_float(a.y[i].y);
+        t[6] = __uint_as_float(a.y[i].z), t[7] = __uint_as_float(a.y[i].w);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] += t[e];
+    }
+  }
+  store_rows<FULL>(reinterpret_cast<T*>(p.C) + row0 * p.ldc + col, p.ldc, row0, p.M, n, v);
+}
+
+template <int ACT, bool FULL>
+__device__ __forceinline__ void bwd_block(const Params& p, const DropKey& key, int row0, int col, int lane,
+                                          const float* st, const Aux& a) {
+  const int n = p.N - col;
+  float v[4][8];
+  staged_rows(st, lane, v);
+  if (ACT != MT_ACT_NONE) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float t[8];
+      unpack8(a.x[i], t);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] *= act_slope<ACT>(t[e]);
+    }
+  }
+  if (p.drop.on) drop_rows(p, key, row0, col, v);  // last: a dropped element is 0 whatever Z holds there
+  if (FULL || n > 0) store_rows<FULL>(reinterpret_cast<bf16*>(p.C) + row0 * p.ldc + col, p.ldc, row0, p.M, n, v);
   if (p.part) {
-    const float s = column_sums32(v, lane);  // rows and columns outside the matrix hold zeros
-    const int first = row - lane, col = col0 + lane;
-    if (first < p.M && col < p.N) p.part[(int64_t)(first >> 5) * p.N + col] = s;
-  }
-}
-
-template <int ACT>
-__device__ __forceinline__ void gated_chunk(const Params& p, int row, int col0, const uint32_t (&a)[32],
-                                            const uint32_t (&b)[32]) {
-  if (row >= p.M) return;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int c = col0 + 8 * j;
-    if (c >= p.N) break;  // N is a multiple of 8
-    float g[8], u[8];
+    float sum[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      g[e] = __uint_as_float(a[8 * j + e]);
-      u[e] = __uint_as_float(b[8 * j + e]);
-    }
-    if (p.gu) {
-      bf16* o = p.gu + row * p.ldgu + c;
-      store8(o, g);
-      store8(o + p.N, u);
+      sum[e] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[e] += FULL || row0 + 8 * i < p.M ? v[i][e] : 0.f;
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) u[e] *= act_value<ACT>(g[e]);
-    store8(reinterpret_cast<bf16*>(p.C) + row * p.ldc + c, u);
+    for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], o);
+    const int first = row0 - (lane >> 2);
+    if (lane < 4 && (FULL || first < p.M)) {
+      float* o = p.part + (int64_t)(first >> 5) * ((p.N + 3) & ~3) + col;  // rows of whole float4s
+      if (FULL || n > 0) reinterpret_cast<float4*>(o)[0] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+      if (FULL || n > 4) reinterpret_cast<float4*>(o)[1] = make_float4(sum[4], sum[5], sum[6], sum[7]);
+    }
   }
 }
 
-template <int ACT>
-__device__ __forceinline__ void gated_bwd_chunk(const Params& p, int row, int col0, const uint32_t (&a)[32]) {
-  if (row >= p.M) return;
+template <int ACT, bool FULL>
+__device__ __forceinline__ void gated_bwd_block(const Params& p, int row0, int col, int lane, const float* st,
+                                                const Aux& a) {
+  if (!FULL && col >= p.N) return;  // N is a multiple of 8
+  float v[4][8];
+  staged_rows(st, lane, v);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int c = col0 + 8 * j;
-    if (c >= p.N) break;  // N is a multiple of 8
+  for (int i = 0; i < 4; ++i) {
+    const int row = row0 + 8 * i;
+    if (!FULL && row >= p.M) break;
     float g[8], u[8], h[8];
-    const bf16* in = p.gu + row * p.ldgu + c;
-    load8(in, g);
-    load8(in + p.N, u);
+    unpack8(a.x[i], g);
+    unpack8(a.y[i], u);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const float dh = __uint_as_float(a[8 * j + e]);
       float value, slope;
       act_both<ACT>(g[e], value, slope);
       h[e] = value * u[e];
-      g[e] = dh * u[e] * slope;
-      u[e] = dh * value;
+      g[e] = v[i][e] * u[e] * slope;
+      u[e] = v[i][e] * value;
     }
-    bf16* o = p.dgu + row * p.lddgu + c;
+    bf16* o = p.dgu + row * p.lddgu + col;
     store8(o, g);
     store8(o + p.N, u);
-    if (p.C) store8(reinterpret_cast<bf16*>(p.C) + row * p.ldc + c, h);
+    if (p.C) store8(reinterpret_cast<bf16*>(p.C) + row * p.ldc + col, h);
   }
 }
 
-// One epilogue warp's share of a tile: OW output columns of 32 rows.
-template <int EPI, int BN, int OW>
-__device__ __forceinline__ void epilogue(const Params& p, const DropKey& key, uint32_t tbase, int row, int col_base,
-                                         int lane) {
-#pragma unroll 1
-  for (int c = 0; c < OW; c += 32) {
-    const int col0 = col_base + c;
-    if (col0 >= p.N) break;
-    uint32_t a[32];
-    tmem_ld_32x32b_x32(tbase + c, a);
-    if (EPI == E_GATED) {
-      uint32_t b[32];
-      tmem_ld_32x32b_x32(tbase + BN / 2 + c, b);
-      tmem_ld_wait();
-      MT_WITH_ACT(p.act, (gated_chunk<ACT>(p, row, col0, a, b)));
-      continue;
+// One block with its activation and fullness as constants.
+template <int EPI>
+__device__ __forceinline__ void block(const Params& p, const DropKey& key, bool full, int row0, int col, int lane,
+                                      const float* st, const Aux& a) {
+  if (full) {
+    if (EPI == E_LINEAR_BF16) MT_WITH_ACT(p.act, (linear_block<ACT, bf16, true>(p, key, row0, col, lane, st, a)));
+    if (EPI == E_LINEAR_F32) MT_WITH_ACT(p.act, (linear_block<ACT, float, true>(p, key, row0, col, lane, st, a)));
+    if (EPI == E_BWD) MT_WITH_ACT(p.act, (bwd_block<ACT, true>(p, key, row0, col, lane, st, a)));
+    if (EPI == E_GATED_BWD) MT_WITH_ACT(p.act, (gated_bwd_block<ACT, true>(p, row0, col, lane, st, a)));
+  } else {
+    if (EPI == E_LINEAR_BF16) MT_WITH_ACT(p.act, (linear_block<ACT, bf16, false>(p, key, row0, col, lane, st, a)));
+    if (EPI == E_LINEAR_F32) MT_WITH_ACT(p.act, (linear_block<ACT, float, false>(p, key, row0, col, lane, st, a)));
+    if (EPI == E_BWD) MT_WITH_ACT(p.act, (bwd_block<ACT, false>(p, key, row0, col, lane, st, a)));
+    if (EPI == E_GATED_BWD) MT_WITH_ACT(p.act, (gated_bwd_block<ACT, false>(p, row0, col, lane, st, a)));
+  }
+}
+
+// Gate and up meet in the registers of a row's lane; their bf16 blocks and h's
+// go through shared memory to be stored.
+template <int ACT>
+__device__ __forceinline__ void gated_block(const Params& p, int row0, int col, int lane, uint4* st,
+                                            const uint32_t (&a)[32], const uint32_t (&b)[32]) {
+  float v[32];
+  const bool in = col < p.N;  // N is a multiple of 8
+  uint4* st2 = st + 128;      // the second half of the warp's buffer
+  if (p.gu) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(a[e]);
+    stage_bf16(st, lane, v);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(b[e]);
+    stage_bf16(st2, lane, v);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int row = row0 + 8 * i, r = (lane >> 2) + 8 * i;
+      if (!in || row >= p.M) break;
+      bf16* o = p.gu + row * p.ldgu + col;
+      *reinterpret_cast<uint4*>(o) = staged_bf16(st, r, lane & 3);
+      *reinterpret_cast<uint4*>(o + p.N) = staged_bf16(st2, r, lane & 3);
     }
-    tmem_ld_wait();
-    if (EPI == E_LINEAR_BF16) {
-      MT_WITH_ACT(p.act, (linear_chunk<ACT, bf16>(p, key, row, col0, a)));
-    } else if (EPI == E_LINEAR_F32) {
-      MT_WITH_ACT(p.act, (linear_chunk<ACT, float>(p, key, row, col0, a)));
-    } else if (EPI == E_BWD) {
-      MT_WITH_ACT(p.act, (bwd_chunk<ACT>(p, key, row, col0, a, lane)));
-    } else if (EPI == E_GATED_BWD) {
-      MT_WITH_ACT(p.act, (gated_bwd_chunk<ACT>(p, row, col0, a)));
-    }
+    __syncwarp();
+  }
+#pragma unroll
+  for (int e = 0; e < 32; ++e) v[e] = act_value<ACT>(__uint_as_float(a[e])) * __uint_as_float(b[e]);
+  stage_bf16(st, lane, v);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int row = row0 + 8 * i, r = (lane >> 2) + 8 * i;
+    if (!in || row >= p.M) break;
+    *reinterpret_cast<uint4*>(reinterpret_cast<bf16*>(p.C) + row * p.ldc + col) = staged_bf16(st, r, lane & 3);
   }
 }
 
@@ -489,13 +587,22 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
     }
   } else {
     // ---------------- epilogue ----------------
-    const int quarter = warp & 3;                 // tensor-memory lanes this warp may read
-    constexpr int OW = ON / (C::EPI_WARPS / 4);   // output columns of this warp's share
+    const int quarter = warp & 3;                // tensor-memory lanes this warp may read
+    constexpr int OW = ON / (C::EPI_WARPS / 4);  // output columns of this warp's share
     const int share = ((warp - 2) >> 2) * OW;
+    float* st = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE_BYTES + 256 + (warp - 2) * EPI_BYTES);
     const DropKey key = drop_key(p.drop);
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int tile = first_tile; tile < num_tiles; tile += tile_step) {
+      int mb, nb;
+      tile_coords(tile, num_m, num_n, mb, nb);
+      const int row0 = mb * C::TILE_M + (int)rank * BM + quarter * 32 + (lane >> 2);  // this lane's first row
+      const int col0 = nb * ON + share;
+      const int blocks = min(OW, p.N - col0 + 31) >> 5;  // none (or less) where the share lies behind the last column
+      const bool full_rows = mb * C::TILE_M + (int)rank * BM + quarter * 32 + 32 <= p.M;
+      Aux aux;  // loaded while the main loop runs
+      if (blocks > 0) load_aux<EPI>(p, full_rows && col0 + 32 <= p.N, row0, col0 + (lane & 3) * 8, aux);
       // warp-uniform outcome: the tcgen05.ld below is warp-collective
       if (__any_sync(0xffffffffu, *abort_flag) ||
           !__all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, limit))) {
@@ -504,18 +611,41 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
         break;
       }
       tc_fence_after();
-      int mb, nb;
-      tile_coords(tile, num_m, num_n, mb, nb);
-      const int row = mb * C::TILE_M + (int)rank * BM + quarter * 32 + lane;
       const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * BN + share;
-      epilogue<EPI, BN, OW>(p, key, tbase, row, nb * ON + share, lane);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (PAIR && rank)
-          mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
-        else
-          mbar_arrive(&tempty[acc]);
+      // Hands the accumulator back as soon as its last columns are in registers.
+      auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR && rank)
+            mbar_arrive_cluster(mapa_shared(smem_u32(&tempty[acc]), 0));
+          else
+            mbar_arrive(&tempty[acc]);
+        }
+      };
+      if (blocks <= 0) release();
+#pragma unroll 1
+      for (int k = 0; k < blocks; ++k) {
+        const int col = col0 + 32 * k + (lane & 3) * 8;  // this lane's first column
+        uint32_t a[32];
+        tmem_ld_32x32b_x32(tbase + 32 * k, a);
+        if (GATED) {
+          uint32_t b[32];
+          tmem_ld_32x32b_x32(tbase + BN / 2 + 32 * k, b);
+          tmem_ld_wait();
+          if (k == blocks - 1) release();
+          MT_WITH_ACT(p.act, (gated_block<ACT>(p, row0, col, lane, reinterpret_cast<uint4*>(st), a, b)));
+        } else {
+          tmem_ld_wait();
+          if (k == blocks - 1) release();
+          stage_f32(st, lane, a);
+          __syncwarp();
+          Aux next;
+          if (k + 1 < blocks) load_aux<EPI>(p, full_rows && col0 + 32 * k + 64 <= p.N, row0, col + 32, next);
+          block<EPI>(p, key, full_rows && col0 + 32 * k + 32 <= p.N, row0, col, lane, st, aux);
+          aux = next;
+        }
+        __syncwarp();  // the buffer is free for the next block
       }
       if (++acc == 2) {
         acc = 0;
@@ -670,7 +800,7 @@ int launch_linear_fwd(const LinearFwd& a, const DropDesc& drop, cudaStream_t st,
   return a.out_type == MT_F32 ? dispatch<false, E_LINEAR_F32>(o, st) : dispatch<false, E_LINEAR_BF16>(o, st);
 }
 
-size_t linear_bwd_partial_floats(int M, int N) { return (size_t)((M + 31) / 32) * N; }
+size_t linear_bwd_partial_floats(int M, int N) { return (size_t)((M + 31) / 32) * ((N + 3) & ~3); }
 
 int launch_linear_bwd_act(const LinearBwd& a, const DropDesc& drop, cudaStream_t st, int* dev_err) {
   Op o{};
@@ -680,7 +810,7 @@ int launch_linear_bwd_act(const LinearBwd& a, const DropDesc& drop, cudaStream_t
   p.Z = (bf16*)a.Z, p.ldz = a.ldz, p.C = a.dZ, p.ldc = a.lddz, p.part = a.db ? a.part : nullptr;
   p.err = dev_err, p.wait_ns = gemm_wait_limit_now();
   if (const int rc = dispatch<true, E_BWD>(o, st)) return rc;
-  return a.db ? launch_column_sums(a.part, (a.M + 31) / 32, a.N, a.N, a.db, a.N, nullptr, st) : MT_OK;
+  return a.db ? launch_column_sums(a.part, (a.M + 31) / 32, (a.N + 3) & ~3, a.N, a.db, a.N, nullptr, st) : MT_OK;
 }
 
 int launch_gated_ffn_fwd(const void* x, int64_t ldx, const void* Wgu, int64_t ldw, int act, void* gu, int64_t ldgu,
