@@ -44,25 +44,49 @@ __device__ __forceinline__ float to_float(bf16 x) { return __bfloat162float(x); 
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(bf16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-// The first n (<= 8) elements at p; zeros behind them.
-template <typename T>
-__device__ __forceinline__ void load8n(const T* p, int n, float (&v)[8]) {
-  if (n >= 8) {
-    load8(p, v);
+// The first n elements at p (all W where n >= W); zeros behind them.
+template <int W, typename T>
+__device__ __forceinline__ void load_n(const T* p, int n, float (&v)[W]) {
+  static_assert(W == 8 || (W == 4 && (sizeof(T) == 4 || sizeof(T) == 2)), "whole vectors");
+  if (n >= W) {
+    if constexpr (W == 8) {
+      load8(p, v);
+    } else if constexpr (sizeof(T) == 4) {
+      const float4 a = *reinterpret_cast<const float4*>(p);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    } else {
+      const uint2 u = *reinterpret_cast<const uint2*>(p);
+      const float2 a = unpack_bf16x2(u.x), b = unpack_bf16x2(u.y);
+      v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+    }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < n ? to_float(p[e]) : 0.f;
+    for (int e = 0; e < W; ++e) v[e] = e < n ? to_float(p[e]) : 0.f;
+  }
+}
+template <int W, typename T>
+__device__ __forceinline__ void store_n(T* p, int n, const float (&v)[W]) {
+  if (n >= W) {
+    if constexpr (W == 8) {
+      store8(p, v);
+    } else if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+      *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < W; ++e)
+      if (e < n) put(p + e, v[e]);
   }
 }
 template <typename T>
+__device__ __forceinline__ void load8n(const T* p, int n, float (&v)[8]) {
+  load_n<8>(p, n, v);
+}
+template <typename T>
 __device__ __forceinline__ void store8n(T* p, int n, const float (&v)[8]) {
-  if (n >= 8) {
-    store8(p, v);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (e < n) put(p + e, v[e]);
-  }
+  store_n<8>(p, n, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -72,20 +96,31 @@ __device__ __forceinline__ void store8n(T* p, int n, const float (&v)[8]) {
 // (1 + tanh u) / 2 = 1 / (1 + exp(-2u)), which keeps its lower tail exact.
 // ReLU passes NaN on; its slope at 0 is 0.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float logistic(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+// 2^x and 1/x to about one unit in the last place, subnormal results flushed
+// (one instruction each; the denormal handling around them costs three more).
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float logistic(float z) { return rcp_fast(1.f + exp2_fast(z * -1.44269504f)); }
 
 // The normal distribution function and exp(-z^2 / 2), which its density and
 // its own approximation share: with x = |z| / sqrt 2 and t = 1 / (1 + p x),
 // erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2) to 1.5e-7 (Abramowitz and Stegun,
-// Handbook of Mathematical Functions, 7.1.26). The lower tail is taken from
-// erfc itself, so nothing cancels there.
+// Handbook of Mathematical Functions, 7.1.26; the coefficients below are
+// halved). The lower tail is taken from erfc itself, so nothing cancels there.
 __device__ __forceinline__ float normal_cdf(float z, float& gauss) {
-  const float x = fabsf(z) * 0.70710678f;
-  const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
-  gauss = __expf(-x * x);
-  const float poly =
-      t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
-  const float q = 0.5f * poly * gauss;
+  const float t = rcp_fast(fmaf(0.3275911f * 0.70710678f, fabsf(z), 1.f));
+  gauss = exp2_fast(z * z * -0.72134752f);
+  const float poly = fmaf(t, fmaf(t, fmaf(t, fmaf(t, 0.5307027145f, -0.7265760135f), 0.7107068705f), -0.142248368f),
+                          0.127414796f);
+  const float q = t * gauss * poly;
   return z < 0.f ? q : 1.f - q;
 }
 

@@ -19,6 +19,8 @@
 // the same BN / 2 rows of Wu: gate and up of an element land in the same lane
 // of tensor memory, BN / 2 columns apart. In a pair of CTAs the first stages
 // the rows of Wg and the second those of Wu.
+#include <type_traits>
+
 #include "act_dropout.cuh"
 
 namespace mt {
@@ -29,23 +31,32 @@ constexpr int BM = 128;
 constexpr int BK = 64;       // 64 bf16 = 128 bytes: one swizzle row
 constexpr int GROUP_M = 16;  // tile raster: 16 M-tiles share a band of N-tiles
 
-// Each epilogue warp's shared memory: 32 rows x 32 columns of fp32.
+// Each epilogue warp's staging buffer: a block of 32 rows x 32 columns of fp32.
 constexpr int EPI_BYTES = 4096;
 
 enum Epi : int { E_LINEAR_BF16, E_LINEAR_F32, E_BWD, E_GATED, E_GATED_BWD };
 
-template <int BN, bool PAIR>
+template <int BN, bool PAIR, int EPI>
 struct Cfg {
   static constexpr int TILE_M = PAIR ? 2 * BM : BM;
-  static constexpr int B_ROWS = PAIR ? BN / 2 : BN;  // rows of B that one CTA stages
+  static constexpr int ON = EPI == E_GATED ? BN / 2 : BN;  // output columns of a tile
+  static constexpr int B_ROWS = PAIR ? BN / 2 : BN;        // rows of B that one CTA stages
   static constexpr int A_BYTES = BM * BK * 2;
   static constexpr int B_BYTES = B_ROWS * BK * 2;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  static constexpr int STAGES = 196608 / STAGE_BYTES < 9 ? 196608 / STAGE_BYTES : 9;  // 192 KB of operands at most
   // Two epilogue warps to a lane quarter once the tile is wide enough to share.
   static constexpr int EPI_WARPS = BN >= 128 ? 8 : 4;
   static constexpr int THREADS = 64 + 32 * EPI_WARPS;
-  static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + 256 + EPI_WARPS * EPI_BYTES;
+  static constexpr int OW = ON / (EPI_WARPS / 4);  // output columns of one epilogue warp
+  // What the epilogue reads beside the accumulator (R, Z, gate and up) is
+  // fetched DEPTH blocks ahead: a block's share is 2 KB to a warp, or 4 KB.
+  static constexpr int AUX_BLOCK = EPI == E_GATED ? 0 : EPI == E_LINEAR_BF16 || EPI == E_BWD ? 2048 : 4096;
+  static constexpr int DEPTH = AUX_BLOCK == 0 ? 1 : OW / 32 < 8192 / AUX_BLOCK ? OW / 32 : 8192 / AUX_BLOCK;
+  static constexpr int EPI_SMEM = EPI_WARPS * (EPI_BYTES + DEPTH * AUX_BLOCK);
+  // As many stages as fit beside them (227 KB), up to 9.
+  static constexpr int ROOM = 232448 - 1024 - 256 - EPI_SMEM;
+  static constexpr int STAGES = ROOM / STAGE_BYTES < 9 ? ROOM / STAGE_BYTES : 9;
+  static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + 256 + EPI_SMEM;
   static constexpr uint32_t TMEM_COLS = 2 * BN;  // 64, 128, 256 or 512
 };
 
@@ -83,8 +94,9 @@ __device__ __forceinline__ void tile_coords(int tile, int num_m, int num_n, int&
 // Epilogues, one warp on 32 rows x 32 columns at a time. tcgen05.ld gives a
 // lane a whole row; storing from there would touch 32 lines with each
 // instruction. So the block goes through shared memory, and each lane handles
-// 8 columns of the rows lane / 4 + 8 i: 64 bytes of a bf16 row (128 of an fp32
-// one) to four neighbouring lanes.
+// 16 bytes of a row beside its neighbours: 8 columns of the rows lane / 4 + 8 i
+// where the output is bf16, 4 columns of the rows lane / 8 + 4 i where it is
+// fp32 (with 8 columns there, each access would take half of every sector).
 // ---------------------------------------------------------------------------
 
 // 16-byte unit u of row r of an fp32 block is kept at u ^ (r % 8), so that
@@ -95,11 +107,14 @@ __device__ __forceinline__ void stage_f32(float* st, int lane, const uint32_t (&
     reinterpret_cast<uint4*>(st)[lane * 8 + (u ^ (lane & 7))] =
         make_uint4(a[4 * u], a[4 * u + 1], a[4 * u + 2], a[4 * u + 3]);
 }
-__device__ __forceinline__ void staged_f32(const float* st, int r, int c8, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(st)[r * 8 + ((2 * c8) ^ (r & 7))];
-  const float4 b = reinterpret_cast<const float4*>(st)[r * 8 + ((2 * c8 + 1) ^ (r & 7))];
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+// W columns of row r, the piece'th from the block's left.
+template <int W>
+__device__ __forceinline__ void staged_f32(const float* st, int r, int piece, float (&v)[W]) {
+#pragma unroll
+  for (int h = 0; h < W / 4; ++h) {
+    const float4 a = reinterpret_cast<const float4*>(st)[r * 8 + ((W / 4 * piece + h) ^ (r & 7))];
+    v[4 * h] = a.x, v[4 * h + 1] = a.y, v[4 * h + 2] = a.z, v[4 * h + 3] = a.w;
+  }
 }
 // The same for a block of bf16, 64 bytes to a row: unit u at u ^ (r / 2 % 4).
 __device__ __forceinline__ void stage_bf16(uint4* st, int lane, const float (&v)[32]) {
@@ -112,10 +127,17 @@ __device__ __forceinline__ void stage_bf16(uint4* st, int lane, const float (&v)
 }
 __device__ __forceinline__ uint4 staged_bf16(const uint4* st, int r, int u) { return st[r * 4 + (u ^ ((r >> 1) & 3))]; }
 
-// What a lane reads beside the accumulator, for its four rows: R (two halves
-// of an fp32 R), Z, or gate and up. It is loaded one block ahead.
+// How a lane's 32 elements of a block lie: NC columns of NR rows, STEP apart.
+template <int EPI>
+struct Lay {
+  static constexpr int NC = EPI == E_LINEAR_F32 ? 4 : 8, NR = 32 / NC, LANES = 32 / NC, STEP = 32 / LANES;
+  static __device__ __forceinline__ int row(int lane) { return lane / LANES; }
+  static __device__ __forceinline__ int col(int lane) { return lane % LANES * NC; }
+};
+
+// What a lane reads beside the accumulator: R, Z, or gate and up.
 struct Aux {
-  uint4 x[4], y[4];
+  uint4 x[8];
 };
 
 // Eight bf16 of which n exist, as they are stored; zeros behind them.
@@ -126,100 +148,130 @@ __device__ __forceinline__ uint4 load8_raw(const bf16* p, int n) {
   return pack8(t);
 }
 
-// FULL: the block lies inside the matrix, so that nothing is tested per element
-// and the four rows' instructions interleave.
-template <int EPI, bool FULL>
+template <int EPI>
+__device__ __forceinline__ bool reads_aux(const Params& p) {
+  return EPI == E_BWD ? p.act != MT_ACT_NONE : EPI == E_GATED_BWD ? true : EPI == E_GATED ? false : p.R != nullptr;
+}
+// Read where it is used, for a block that the matrix ends in.
+template <int EPI>
 __device__ __forceinline__ void load_aux(const Params& p, int row0, int col, Aux& a) {
-  const int n = FULL ? 8 : p.N - col;
-  if (!FULL && n <= 0) return;
-  const bool wanted = EPI == E_BWD ? p.act != MT_ACT_NONE : EPI == E_GATED_BWD ? true : p.R != nullptr;
-  if (EPI == E_GATED || !wanted) return;
+  using L = Lay<EPI>;
+  const int n = p.N - col;
+  if (!reads_aux<EPI>(p) || n <= 0) return;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = row0 + 8 * i;
-    if (!FULL && row >= p.M) break;
+  for (int i = 0; i < L::NR; ++i) {
+    const int row = row0 + L::STEP * i;
+    if (row >= p.M) break;
     if (EPI == E_LINEAR_BF16) {
       a.x[i] = load8_raw(reinterpret_cast<const bf16*>(p.R) + row * p.ldr + col, n);
     } else if (EPI == E_LINEAR_F32) {
-      float t[8];
-      load8n(reinterpret_cast<const float*>(p.R) + row * p.ldr + col, n, t);
+      float t[4];
+      load_n<4>(reinterpret_cast<const float*>(p.R) + row * p.ldr + col, n, t);
       a.x[i] = make_uint4(__float_as_uint(t[0]), __float_as_uint(t[1]), __float_as_uint(t[2]), __float_as_uint(t[3]));
-      a.y[i] = make_uint4(__float_as_uint(t[4]), __float_as_uint(t[5]), __float_as_uint(t[6]), __float_as_uint(t[7]));
     } else if (EPI == E_BWD) {
       a.x[i] = load8_raw(p.Z + row * p.ldz + col, n);
-    } else if (EPI == E_GATED_BWD) {
+    } else {
       const bf16* g = p.gu + row * p.ldgu + col;  // N is a multiple of 8
-      a.x[i] = *reinterpret_cast<const uint4*>(g);
-      a.y[i] = *reinterpret_cast<const uint4*>(g + p.N);
+      a.x[2 * i] = *reinterpret_cast<const uint4*>(g);
+      a.x[2 * i + 1] = *reinterpret_cast<const uint4*>(g + p.N);
+    }
+  }
+}
+
+// The same for a block inside the matrix, ahead of time and into shared memory:
+// a lane copies the very pieces that it reads back itself, so nothing but its
+// own copies has to be waited for.
+template <int EPI>
+__device__ __forceinline__ void fetch_aux(const Params& p, uint32_t slot, int row0, int col) {
+  using L = Lay<EPI>;
+  if (!reads_aux<EPI>(p)) return;
+#pragma unroll
+  for (int i = 0; i < L::NR; ++i) {
+    const int row = row0 + L::STEP * i;
+    if (EPI == E_LINEAR_BF16) {
+      copy16(slot + i * 512, reinterpret_cast<const bf16*>(p.R) + row * p.ldr + col);
+    } else if (EPI == E_LINEAR_F32) {
+      copy16(slot + i * 512, reinterpret_cast<const float*>(p.R) + row * p.ldr + col);
+    } else if (EPI == E_BWD) {
+      copy16(slot + i * 512, p.Z + row * p.ldz + col);
+    } else {
+      const bf16* g = p.gu + row * p.ldgu + col;
+      copy16(slot + i * 1024, g);
+      copy16(slot + i * 1024 + 512, g + p.N);
     }
   }
 }
 template <int EPI>
-__device__ __forceinline__ void load_aux(const Params& p, bool full, int row0, int col, Aux& a) {
-  if (full)
-    load_aux<EPI, true>(p, row0, col, a);
-  else
-    load_aux<EPI, false>(p, row0, col, a);
+__device__ __forceinline__ void fetched_aux(const uint4* slot, Aux& a) {
+#pragma unroll
+  for (int i = 0; i < (EPI == E_LINEAR_BF16 || EPI == E_BWD ? 4 : 8); ++i) a.x[i] = slot[i * 32];
 }
 
-// The lane's rows of the staged block; rows and columns outside the matrix
+// The lane's part of the staged block; rows and columns outside the matrix
 // hold what the product of zeros left there.
-__device__ __forceinline__ void staged_rows(const float* st, int lane, float (&v)[4][8]) {
+template <int EPI, int NR, int NC>
+__device__ __forceinline__ void staged_rows(const float* st, int lane, float (&v)[NR][NC]) {
+  using L = Lay<EPI>;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) staged_f32(st, (lane >> 2) + 8 * i, lane & 3, v[i]);
+  for (int i = 0; i < NR; ++i) staged_f32<NC>(st, L::row(lane) + L::STEP * i, lane % L::LANES, v[i]);
 }
-__device__ __forceinline__ void drop_rows(const Params& p, const DropKey& key, int row0, int col, float (&v)[4][8]) {
+template <int EPI, int NR, int NC>
+__device__ __forceinline__ void drop_rows(const Params& p, const DropKey& key, int row0, int col, float (&v)[NR][NC]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    drop4(v[i], col >> 2, p.drop.row0 + (uint32_t)(row0 + 8 * i), p.drop, key);
-    drop4(v[i] + 4, (col >> 2) + 1, p.drop.row0 + (uint32_t)(row0 + 8 * i), p.drop, key);
-  }
+  for (int i = 0; i < NR; ++i)
+#pragma unroll
+    for (int h = 0; h < NC / 4; ++h)
+      drop4(v[i] + 4 * h, (col >> 2) + h, p.drop.row0 + (uint32_t)(row0 + Lay<EPI>::STEP * i), p.drop, key);
 }
-template <bool FULL, typename T>
-__device__ __forceinline__ void store_rows(T* out, int64_t ld, int row0, int M, int n, const float (&v)[4][8]) {
+template <int EPI, bool FULL, int NR, int NC, typename T>
+__device__ __forceinline__ void store_rows(T* out, int64_t ld, int row0, int M, int n, const float (&v)[NR][NC]) {
+  using L = Lay<EPI>;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (FULL || row0 + 8 * i < M) store8n(out + i * 8 * ld, FULL ? 8 : n, v[i]);
+  for (int i = 0; i < NR; ++i)
+    if (FULL || row0 + L::STEP * i < M) store_n<NC>(out + i * L::STEP * ld, FULL ? NC : n, v[i]);
 }
 
-template <int ACT, typename T, bool FULL>
+// FULL: the block lies inside the matrix, so that nothing is tested per element
+// and the rows' instructions interleave.
+template <int EPI, int ACT, bool FULL>
 __device__ __forceinline__ void linear_block(const Params& p, const DropKey& key, int row0, int col, int lane,
                                              const float* st, const Aux& a) {
+  using L = Lay<EPI>;
+  using T = std::conditional_t<EPI == E_LINEAR_F32, float, bf16>;
+  constexpr int NR = L::NR, NC = L::NC;
   const int n = p.N - col;
   if (!FULL && n <= 0) return;
-  float v[4][8];
-  staged_rows(st, lane, v);
+  float v[NR][NC];
+  staged_rows<EPI>(st, lane, v);
   if (p.bias) {
-    float bias[8];
-    load8n(p.bias + col, FULL ? 8 : n, bias);
+    float bias[NC];
+    load_n<NC>(p.bias + col, FULL ? NC : n, bias);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < NR; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] += bias[e];
+      for (int e = 0; e < NC; ++e) v[i][e] += bias[e];
   }
-  if (p.Z) store_rows<FULL>(p.Z + row0 * p.ldz + col, p.ldz, row0, p.M, n, v);
+  if (p.Z) store_rows<EPI, FULL>(p.Z + row0 * p.ldz + col, p.ldz, row0, p.M, n, v);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < NR; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[i][e] = act_value<ACT>(v[i][e]);
-  if (p.drop.on) drop_rows(p, key, row0, col, v);
+    for (int e = 0; e < NC; ++e) v[i][e] = act_value<ACT>(v[i][e]);
+  if (p.drop.on) drop_rows<EPI>(p, key, row0, col, v);
   if (p.R) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float t[8];
-      if (sizeof(T) == 2) {
+    for (int i = 0; i < NR; ++i) {
+      float t[NC];
+      if constexpr (NC == 8) {
         unpack8(a.x[i], t);
       } else {
         t[0] = __uint_as_float(a.x[i].x), t[1] = __uint_as_float(a.x[i].y);
         t[2] = __uint_as_float(a.x[i].z), t[3] = __uint_as_float(a.x[i].w);
-        t[4] = __uint_as_float(a.y[i].x), t[5] = __uint_as_float(a.y[i].y);
-        t[6] = __uint_as_float(a.y[i].z), t[7] = __uint_as_float(a.y[i].w);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] += t[e];
+      for (int e = 0; e < NC; ++e) v[i][e] += t[e];
     }
   }
-  store_rows<FULL>(reinterpret_cast<T*>(p.C) + row0 * p.ldc + col, p.ldc, row0, p.M, n, v);
+  store_rows<EPI, FULL>(reinterpret_cast<T*>(p.C) + row0 * p.ldc + col, p.ldc, row0, p.M, n, v);
 }
 
 template <int ACT, bool FULL>
@@ -227,7 +279,7 @@ __device__ __forceinline__ void bwd_block(const Params& p, const DropKey& key, i
                                           const float* st, const Aux& a) {
   const int n = p.N - col;
   float v[4][8];
-  staged_rows(st, lane, v);
+  staged_rows<E_BWD>(st, lane, v);
   if (ACT != MT_ACT_NONE) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -237,8 +289,8 @@ __device__ __forceinline__ void bwd_block(const Params& p, const DropKey& key, i
       for (int e = 0; e < 8; ++e) v[i][e] *= act_slope<ACT>(t[e]);
     }
   }
-  if (p.drop.on) drop_rows(p, key, row0, col, v);  // last: a dropped element is 0 whatever Z holds there
-  if (FULL || n > 0) store_rows<FULL>(reinterpret_cast<bf16*>(p.C) + row0 * p.ldc + col, p.ldc, row0, p.M, n, v);
+  if (p.drop.on) drop_rows<E_BWD>(p, key, row0, col, v);  // last: a dropped element is 0 whatever Z holds there
+  if (FULL || n > 0) store_rows<E_BWD, FULL>(reinterpret_cast<bf16*>(p.C) + row0 * p.ldc + col, p.ldc, row0, p.M, n, v);
   if (p.part) {
     float sum[8];
 #pragma unroll
@@ -265,14 +317,14 @@ __device__ __forceinline__ void gated_bwd_block(const Params& p, int row0, int c
                                                 const Aux& a) {
   if (!FULL && col >= p.N) return;  // N is a multiple of 8
   float v[4][8];
-  staged_rows(st, lane, v);
+  staged_rows<E_GATED_BWD>(st, lane, v);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = row0 + 8 * i;
     if (!FULL && row >= p.M) break;
     float g[8], u[8], h[8];
-    unpack8(a.x[i], g);
-    unpack8(a.y[i], u);
+    unpack8(a.x[2 * i], g);
+    unpack8(a.x[2 * i + 1], u);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       float value, slope;
@@ -293,13 +345,13 @@ template <int EPI>
 __device__ __forceinline__ void block(const Params& p, const DropKey& key, bool full, int row0, int col, int lane,
                                       const float* st, const Aux& a) {
   if (full) {
-    if (EPI == E_LINEAR_BF16) MT_WITH_ACT(p.act, (linear_block<ACT, bf16, true>(p, key, row0, col, lane, st, a)));
-    if (EPI == E_LINEAR_F32) MT_WITH_ACT(p.act, (linear_block<ACT, float, true>(p, key, row0, col, lane, st, a)));
+    if (EPI == E_LINEAR_BF16) MT_WITH_ACT(p.act, (linear_block<E_LINEAR_BF16, ACT, true>(p, key, row0, col, lane, st, a)));
+    if (EPI == E_LINEAR_F32) MT_WITH_ACT(p.act, (linear_block<E_LINEAR_F32, ACT, true>(p, key, row0, col, lane, st, a)));
     if (EPI == E_BWD) MT_WITH_ACT(p.act, (bwd_block<ACT, true>(p, key, row0, col, lane, st, a)));
     if (EPI == E_GATED_BWD) MT_WITH_ACT(p.act, (gated_bwd_block<ACT, true>(p, row0, col, lane, st, a)));
   } else {
-    if (EPI == E_LINEAR_BF16) MT_WITH_ACT(p.act, (linear_block<ACT, bf16, false>(p, key, row0, col, lane, st, a)));
-    if (EPI == E_LINEAR_F32) MT_WITH_ACT(p.act, (linear_block<ACT, float, false>(p, key, row0, col, lane, st, a)));
+    if (EPI == E_LINEAR_BF16) MT_WITH_ACT(p.act, (linear_block<E_LINEAR_BF16, ACT, false>(p, key, row0, col, lane, st, a)));
+    if (EPI == E_LINEAR_F32) MT_WITH_ACT(p.act, (linear_block<E_LINEAR_F32, ACT, false>(p, key, row0, col, lane, st, a)));
     if (EPI == E_BWD) MT_WITH_ACT(p.act, (bwd_block<ACT, false>(p, key, row0, col, lane, st, a)));
     if (EPI == E_GATED_BWD) MT_WITH_ACT(p.act, (gated_bwd_block<ACT, false>(p, row0, col, lane, st, a)));
   }
@@ -353,12 +405,12 @@ __device__ __forceinline__ void gated_block(const Params& p, int row0, int col, 
 // gated product and unused otherwise.
 // ---------------------------------------------------------------------------
 template <int BN, bool PAIR, bool B_MN, int EPI>
-__global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
+__global__ void __launch_bounds__(Cfg<BN, PAIR, EPI>::THREADS, 1)
     k_linear(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
              const __grid_constant__ CUtensorMap tmB2, const __grid_constant__ Params p) {
-  using C = Cfg<BN, PAIR>;
+  using C = Cfg<BN, PAIR, EPI>;
   constexpr bool GATED = EPI == E_GATED;
-  constexpr int ON = GATED ? BN / 2 : BN;  // output columns of a tile
+  constexpr int ON = C::ON;
   static_assert(!B_MN || BN >= 64, "an MN-major operand is staged 64 columns at a time");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -588,21 +640,30 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
   } else {
     // ---------------- epilogue ----------------
     const int quarter = warp & 3;                // tensor-memory lanes this warp may read
-    constexpr int OW = ON / (C::EPI_WARPS / 4);  // output columns of this warp's share
-    const int share = ((warp - 2) >> 2) * OW;
-    float* st = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE_BYTES + 256 + (warp - 2) * EPI_BYTES);
+    const int share = ((warp - 2) >> 2) * C::OW;
+    uint8_t* mine = smem + C::STAGES * C::STAGE_BYTES + 256;
+    float* st = reinterpret_cast<float*>(mine + (warp - 2) * EPI_BYTES);
+    const uint4* fetched = reinterpret_cast<uint4*>(mine + C::EPI_WARPS * EPI_BYTES + (warp - 2) * C::DEPTH * C::AUX_BLOCK) + lane;
     const DropKey key = drop_key(p.drop);
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int tile = first_tile; tile < num_tiles; tile += tile_step) {
       int mb, nb;
       tile_coords(tile, num_m, num_n, mb, nb);
-      const int row0 = mb * C::TILE_M + (int)rank * BM + quarter * 32 + (lane >> 2);  // this lane's first row
+      const int row0 = mb * C::TILE_M + (int)rank * BM + quarter * 32 + Lay<EPI>::row(lane);  // this lane's first row
       const int col0 = nb * ON + share;
-      const int blocks = min(OW, p.N - col0 + 31) >> 5;  // none (or less) where the share lies behind the last column
+      const int blocks = min(C::OW, p.N - col0 + 31) >> 5;  // none (or less) where the share lies behind the last column
       const bool full_rows = mb * C::TILE_M + (int)rank * BM + quarter * 32 + 32 <= p.M;
-      Aux aux;  // loaded while the main loop runs
-      if (blocks > 0) load_aux<EPI>(p, full_rows && col0 + 32 <= p.N, row0, col0 + (lane & 3) * 8, aux);
+      auto inside = [&](int k) { return full_rows && col0 + 32 * k + 32 <= p.N; };
+      // One group of copies to a block, empty where there is nothing to copy.
+      auto fetch = [&](int k) {
+        if (C::AUX_BLOCK == 0) return;
+        if (k < blocks && inside(k))
+          fetch_aux<EPI>(p, smem_u32(fetched) + k % C::DEPTH * C::AUX_BLOCK, row0, col0 + 32 * k + Lay<EPI>::col(lane));
+        copy_commit();
+      };
+#pragma unroll
+      for (int k = 0; k < C::DEPTH; ++k) fetch(k);  // while the main loop runs
       // warp-uniform outcome: the tcgen05.ld below is warp-collective
       if (__any_sync(0xffffffffu, *abort_flag) ||
           !__all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, limit))) {
@@ -626,7 +687,7 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
       if (blocks <= 0) release();
 #pragma unroll 1
       for (int k = 0; k < blocks; ++k) {
-        const int col = col0 + 32 * k + (lane & 3) * 8;  // this lane's first column
+        const int col = col0 + 32 * k + Lay<EPI>::col(lane);  // this lane's first column
         uint32_t a[32];
         tmem_ld_32x32b_x32(tbase + 32 * k, a);
         if (GATED) {
@@ -640,10 +701,16 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
           if (k == blocks - 1) release();
           stage_f32(st, lane, a);
           __syncwarp();
-          Aux next;
-          if (k + 1 < blocks) load_aux<EPI>(p, full_rows && col0 + 32 * k + 64 <= p.N, row0, col + 32, next);
-          block<EPI>(p, key, full_rows && col0 + 32 * k + 32 <= p.N, row0, col, lane, st, aux);
-          aux = next;
+          Aux aux;
+          if (C::AUX_BLOCK > 0) {
+            copy_wait<C::DEPTH - 1>();
+            if (inside(k))
+              fetched_aux<EPI>(fetched + k % C::DEPTH * (C::AUX_BLOCK / 16), aux);
+            else
+              load_aux<EPI>(p, row0, col, aux);
+          }
+          block<EPI>(p, key, inside(k), row0, col, lane, st, aux);
+          fetch(k + C::DEPTH);
         }
         __syncwarp();  // the buffer is free for the next block
       }
@@ -652,6 +719,7 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR>::THREADS, 1)
         acc_phase ^= 1;
       }
     }
+    copy_wait<0>();  // also where the loop was left early
   }
 
   tc_fence_before();
@@ -686,9 +754,9 @@ struct Op {
 
 template <int BN, bool PAIR, bool B_MN, int EPI>
 int launch(const Op& o, int device, int num_sms, cudaStream_t st) {
-  using C = Cfg<BN, PAIR>;
+  using C = Cfg<BN, PAIR, EPI>;
   constexpr bool GATED = EPI == E_GATED;
-  constexpr int ON = GATED ? BN / 2 : BN;
+  constexpr int ON = C::ON;
   auto kernel = k_linear<BN, PAIR, B_MN, EPI>;
   const Params& p = o.p;
   CUtensorMap ta, tb, tb2;
@@ -771,7 +839,7 @@ int dispatch(const Op& o, cudaStream_t st) {
   if (family != 1) consider(0, 256, true);
   if (family != 1) consider(1, 128, true);
   if (family != 2) {
-    consider(2, 256, false);
+    if (G == 2) consider(2, 256, false);
     consider(3, 128, false);
     consider(4, 64, false);
     if (!B_MN && G == 1) consider(5, 32, false);
@@ -779,13 +847,15 @@ int dispatch(const Op& o, cudaStream_t st) {
   switch (best) {
     case 0: return launch<256, true, B_MN, EPI>(o, device, sms, st);
     case 1: return launch<128, true, B_MN, EPI>(o, device, sms, st);
-    case 2: return launch<256, false, B_MN, EPI>(o, device, sms, st);
     case 3: return launch<128, false, B_MN, EPI>(o, device, sms, st);
     case 4: return launch<64, false, B_MN, EPI>(o, device, sms, st);
-    default:
+    case 5:
       if constexpr (!B_MN && G == 1) return launch<32, false, B_MN, EPI>(o, device, sms, st);
-      return MT_ERR_ARG;
+      break;
+    default:
+      if constexpr (G == 2) return launch<256, false, B_MN, EPI>(o, device, sms, st);
   }
+  return MT_ERR_CONFIG;  // not reached
 }
 
 }  // namespace
