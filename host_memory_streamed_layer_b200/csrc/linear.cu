@@ -557,8 +557,12 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI>::THREADS, 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       // ---------------- MMA issuer ----------------
+      // The whole warp walks the loop and one elected lane issues: with the
+      // loop inside one lane's branch, every MMA and commit first moved its
+      // operands to uniform registers, and a k-block took 560 cycles and more
+      // to issue where the tensor core needs 512.
       constexpr uint32_t idesc = idesc_bf16_f32(C::TILE_M, BN, false, B_MN);
       // Descriptors of stage 0; stages and k-steps only move the start address.
       const uint32_t s0 = smem_u32(smem);
@@ -566,8 +570,8 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI>::THREADS, 1)
       const uint64_t b0 = sdesc_sw128(s0 + C::A_BYTES, B_MN ? 8192 : 16, 1024);
       constexpr uint32_t kStage = C::STAGE_BYTES >> 4;
       constexpr uint32_t kAStep = 32 >> 4, kBStep = (B_MN ? 2048 : 32) >> 4;
-      const uint32_t full0 = smem_u32(&full[0]), empty0 = smem_u32(&empty[0]);
-      const uint32_t empty0_peer = PAIR ? mapa_shared(empty0, 1) : 0;
+      const uint32_t full0 = smem_u32(&full[0]), empty0 = smem_u32(&empty[0]), tfull0 = smem_u32(&tfull[0]);
+      const uint32_t empty0_peer = PAIR ? mapa_shared(empty0, 1) : 0, tfull0_peer = PAIR ? mapa_shared(tfull0, 1) : 0;
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
@@ -577,64 +581,70 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI>::THREADS, 1)
       for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
         const bool free_acc = PAIR ? mbar_wait_cluster(&tempty[acc], acc_phase ^ 1)
                                    : mbar_wait(&tempty[acc], acc_phase ^ 1, limit);
-        if (*abort_flag || !free_acc) {
+        if (!__all_sync(0xffffffffu, free_acc && !*abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
         for (int kb = 0; kb < num_kb; ++kb) {
-          if (!mbar_wait_u32(full0 + 8 * stage, phase, limit)) {
+          if (!__all_sync(0xffffffffu, mbar_wait_u32(full0 + 8 * stage, phase, limit))) {
             ok = false;
             break;
           }
           // The stage's bytes were written by TMA and published through this
           // mbarrier, which orders them for the MMAs' reads: no tcgen05 fence.
           const uint64_t ad = a0 + stage * kStage, bd = b0 + stage * kStage;
+          if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            if (PAIR)
-              umma_bf16_pair(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, (kb | kk) != 0);
-            else
-              umma_bf16(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, (kb | kk) != 0);
+            for (int kk = 0; kk < BK / 16; ++kk) {
+              if (PAIR)
+                umma_bf16_pair(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, (kb | kk) != 0);
+              else
+                umma_bf16(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, (kb | kk) != 0);
+            }
+            if (PAIR) {
+              umma_commit_pair(empty0 + 8 * stage);
+              umma_commit_pair(empty0_peer + 8 * stage);
+            } else {
+              umma_commit_u32(empty0 + 8 * stage);
+            }
+            if (kb == num_kb - 1) {
+              if (PAIR) {
+                umma_commit_pair(tfull0 + 8 * acc);
+                umma_commit_pair(tfull0_peer + 8 * acc);
+              } else {
+                umma_commit_u32(tfull0 + 8 * acc);
+              }
+            }
           }
           issued = true;
-          if (PAIR) {
-            umma_commit_pair(empty0 + 8 * stage);
-            umma_commit_pair(empty0_peer + 8 * stage);
-          } else {
-            umma_commit_u32(empty0 + 8 * stage);
-          }
           if (++stage == C::STAGES) {
             stage = 0;
             phase ^= 1;
           }
         }
         if (!ok) break;
-        if (PAIR) {
-          const uint32_t tb = smem_u32(&tfull[acc]);
-          umma_commit_pair(tb);
-          umma_commit_pair(mapa_shared(tb, 1));
-        } else {
-          umma_commit(&tfull[acc]);
-        }
         if (++acc == 2) {
           acc = 0;
           acc_phase ^= 1;
         }
       }
-      if (!ok) {
+      if (!ok && lane == 0) {
         record_error(p.err, DEV_TIMEOUT_MMA);
         *abort_flag = 1;
       }
       // Every MMA issued here completes before tensor memory is freed, also
       // when the epilogue gave up on an accumulator it will never read.
       if (issued) {
-        if (PAIR)
-          umma_commit_pair(smem_u32(drain));
-        else
-          umma_commit(drain);
-        if (!mbar_wait(drain, 0)) record_error(p.err, DEV_TIMEOUT_TEARDOWN);
+        if (elect_one()) {
+          if (PAIR)
+            umma_commit_pair(smem_u32(drain));
+          else
+            umma_commit(drain);
+        }
+        __syncwarp();
+        if (!mbar_wait(drain, 0) && lane == 0) record_error(p.err, DEV_TIMEOUT_TEARDOWN);
       }
     }
   } else {
