@@ -468,30 +468,30 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI>::THREADS, 1)
   const int tile_step = PAIR ? gridDim.x >> 1 : gridDim.x;
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ---------------- TMA producer ----------------
-      int stage = 0;
-      uint32_t phase = 0;
-      int issued = 0;  // stages filled so far (for the teardown)
-      const uint32_t fb0 = PAIR ? mapa_shared(smem_u32(&full[0]), 0) : 0;  // the leader's full barriers
-      bool ok = true;
-      for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
-        int mb, nb;
-        tile_coords(tile, num_m, num_n, mb, nb);
-        const int m0 = mb * C::TILE_M + (int)rank * BM;
-        // A pair's B rows are split over its CTAs; a gated tile has one half from each weight.
-        const int n0 = nb * ON + (PAIR && !GATED ? (int)rank * (BN / 2) : 0);
-        const CUtensorMap* mB = PAIR && GATED && rank ? &tmB2 : &tmB;
-        for (int kb = 0; kb < num_kb; ++kb) {
-          if (*abort_flag || !mbar_wait(&empty[stage], phase ^ 1, limit)) {
-            record_error(p.err, DEV_TIMEOUT_PRODUCER);
-            *abort_flag = 1;
-            ok = false;
-            break;
-          }
-          uint8_t* sa = smem + stage * C::STAGE_BYTES;
-          uint8_t* sb = sa + C::A_BYTES;
-          const int k0 = kb * BK;
+    // ---------------- TMA producer (the whole warp; one elected lane copies) ----------------
+    int stage = 0;
+    uint32_t phase = 0;
+    int issued = 0;  // stages filled so far (for the teardown)
+    const uint32_t fb0 = PAIR ? mapa_shared(smem_u32(&full[0]), 0) : 0;  // the leader's full barriers
+    const uint32_t empty0 = smem_u32(&empty[0]);
+    bool ok = true;
+    for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
+      int mb, nb;
+      tile_coords(tile, num_m, num_n, mb, nb);
+      const int m0 = mb * C::TILE_M + (int)rank * BM;
+      // A pair's B rows are split over its CTAs; a gated tile has one half from each weight.
+      const int n0 = nb * ON + (PAIR && !GATED ? (int)rank * (BN / 2) : 0);
+      const CUtensorMap* mB = PAIR && GATED && rank ? &tmB2 : &tmB;
+      for (int kb = 0; kb < num_kb; ++kb) {
+        const bool got = mbar_wait_u32(empty0 + 8 * stage, phase ^ 1, limit);
+        if (!__all_sync(0xffffffffu, got && !*abort_flag)) {
+          ok = false;
+          break;
+        }
+        uint8_t* sa = smem + stage * C::STAGE_BYTES;
+        uint8_t* sb = sa + C::A_BYTES;
+        const int k0 = kb * BK;
+        if (elect_one()) {
           if (PAIR) {
             const uint32_t fb = fb0 + 8 * stage;
             if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::STAGE_BYTES);
@@ -515,13 +515,20 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI>::THREADS, 1)
               for (int i = 0; i < C::B_ROWS / 64; ++i) tma_load_2d(sb + i * 8192, &tmB, &full[stage], n0 + i * 64, k0);
             }
           }
-          ++issued;
-          if (++stage == C::STAGES) {
-            stage = 0;
-            phase ^= 1;
-          }
+        }
+        ++issued;
+        if (++stage == C::STAGES) {
+          stage = 0;
+          phase ^= 1;
         }
       }
+    }
+    if (!ok && lane == 0) {
+      record_error(p.err, DEV_TIMEOUT_PRODUCER);
+      *abort_flag = 1;
+    }
+    __syncwarp();
+    if (lane == 0) {
       if (ok) {
         // Wait until the MMA has released every stage, so that no commit is on
         // its way to this CTA's barriers when it exits. If another role gives
@@ -556,6 +563,7 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI>::THREADS, 1)
         }
       }
     }
+    __syncwarp();
   } else if (warp == 1) {
     if (rank == 0) {
       // ---------------- MMA issuer ----------------
@@ -571,7 +579,6 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI>::THREADS, 1)
       constexpr uint32_t kStage = C::STAGE_BYTES >> 4;
       constexpr uint32_t kAStep = 32 >> 4, kBStep = (B_MN ? 2048 : 32) >> 4;
       const uint32_t full0 = smem_u32(&full[0]), empty0 = smem_u32(&empty[0]), tfull0 = smem_u32(&tfull[0]);
-      const uint32_t empty0_peer = PAIR ? mapa_shared(empty0, 1) : 0, tfull0_peer = PAIR ? mapa_shared(tfull0, 1) : 0;
       int stage = 0;
       uint32_t phase = 0;
       int acc = 0;
@@ -603,19 +610,15 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI>::THREADS, 1)
               else
                 umma_bf16(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, (kb | kk) != 0);
             }
-            if (PAIR) {
-              umma_commit_pair(empty0 + 8 * stage);
-              umma_commit_pair(empty0_peer + 8 * stage);
-            } else {
+            if (PAIR)
+              umma_commit_both(empty0 + 8 * stage);
+            else
               umma_commit_u32(empty0 + 8 * stage);
-            }
             if (kb == num_kb - 1) {
-              if (PAIR) {
-                umma_commit_pair(tfull0 + 8 * acc);
-                umma_commit_pair(tfull0_peer + 8 * acc);
-              } else {
+              if (PAIR)
+                umma_commit_both(tfull0 + 8 * acc);
+              else
                 umma_commit_u32(tfull0 + 8 * acc);
-              }
             }
           }
           issued = true;
