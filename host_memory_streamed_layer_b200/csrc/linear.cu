@@ -51,7 +51,7 @@ struct Cfg {
   // What the epilogue reads beside the accumulator (R, Z, gate and up) is
   // fetched DEPTH blocks ahead: a block's share is 2 KB to a warp, or 4 KB.
   static constexpr int AUX_BLOCK = EPI == E_GATED ? 0 : EPI == E_LINEAR_BF16 || EPI == E_BWD ? 2048 : 4096;
-  static constexpr int DEPTH = AUX_BLOCK == 0 ? 1 : OW / 32 < 8192 / AUX_BLOCK ? OW / 32 : 8192 / AUX_BLOCK;
+  static constexpr int DEPTH = AUX_BLOCK == 0 ? 1 : OW / 32 < 4096 / AUX_BLOCK ? OW / 32 : 4096 / AUX_BLOCK;
   static constexpr int EPI_SMEM = EPI_WARPS * (EPI_BYTES + DEPTH * AUX_BLOCK);
   // As many stages as fit beside them (227 KB), up to 9.
   static constexpr int ROOM = 232448 - 1024 - 256 - EPI_SMEM;
