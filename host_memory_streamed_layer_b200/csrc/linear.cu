@@ -36,31 +36,32 @@ constexpr int EPI_BYTES = 4096;
 
 enum Epi : int { E_LINEAR_BF16, E_LINEAR_F32, E_BWD, E_GATED, E_GATED_BWD };
 
-template <int BN, bool PAIR, int EPI>
-struct Cfg {
-  static constexpr int TILE_M = PAIR ? 2 * BM : BM;
-  static constexpr int ON = EPI == E_GATED ? BN / 2 : BN;  // output columns of a tile
-  static constexpr int B_ROWS = PAIR ? BN / 2 : BN;        // rows of B that one CTA stages
-  static constexpr int A_BYTES = BM * BK * 2;
-  static constexpr int B_BYTES = B_ROWS * BK * 2;
-  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-  // Two epilogue warps to a lane quarter once the tile is wide enough to share.
-  static constexpr int EPI_WARPS = BN >= 128 ? 8 : 4;
-  static constexpr int THREADS = 64 + 32 * EPI_WARPS;
-  static constexpr int OW = ON / (EPI_WARPS / 4);  // output columns of one epilogue warp
-  // What the epilogue reads beside the accumulator (R, Z, gate and up) is
-  // fetched DEPTH blocks ahead: a block's share is 2 KB to a warp, or 4 KB.
-  static constexpr int AUX_BLOCK = EPI == E_GATED ? 0 : EPI == E_LINEAR_BF16 || EPI == E_BWD ? 2048 : 4096;
-  static constexpr int DEPTH = AUX_BLOCK == 0 ? 1 : OW / 32 < 4096 / AUX_BLOCK ? OW / 32 : 4096 / AUX_BLOCK;
-  static constexpr int EPI_SMEM = EPI_WARPS * (EPI_BYTES + DEPTH * AUX_BLOCK);
-  // As many stages as fit beside them (227 KB), up to 9.
-  static constexpr int ROOM = 232448 - 1024 - 256 - EPI_SMEM;
-  static constexpr int STAGES = ROOM / STAGE_BYTES < 9 ? ROOM / STAGE_BYTES : 9;
-  static constexpr int SMEM = 1024 + STAGES * STAGE_BYTES + 256 + EPI_SMEM;
-  static constexpr uint32_t TMEM_COLS = 2 * BN;  // 64, 128, 256 or 512
+// Epilogue warps: two to a lane quarter, each taking every other block of 32
+// columns.
+constexpr int EPI_WARPS = 8;
+constexpr int THREADS = 64 + 32 * EPI_WARPS;
+constexpr int SMEM_MOST = 232448;  // 227 KB
+constexpr int BAR_BYTES = 256;     // barriers of at most 12 stages
+constexpr int MAX_STAGES = 12;
+constexpr uint32_t TMEM_COLS = 512;  // two accumulators of up to 256 columns
+
+// What the epilogue reads beside the accumulator (R, Z, gate and up) is
+// fetched DEPTH blocks ahead: a block's share is 2 KB to a warp, or 4 KB.
+template <int EPI>
+struct Ahead {
+  static constexpr int BLOCK = EPI == E_GATED ? 0 : EPI == E_LINEAR_BF16 || EPI == E_BWD ? 2048 : 4096;
+  static constexpr int DEPTH = BLOCK == 0 ? 1 : 4096 / BLOCK;
+};
+
+// The tile and the pipeline of a launch, chosen by the host. A tile is 128
+// rows (256 for a pair of CTAs) by bn columns; a stage holds a_rows rows of A
+// and b_rows of B, 64 deep.
+struct Tile {
+  int bn, a_rows, b_rows, stages;
 };
 
 struct Params {
+  Tile t;
   int M, N, K;  // N: columns of the output (of each of gate and up)
   int act;
   DropDesc drop;
@@ -154,9 +155,9 @@ __device__ __forceinline__ bool reads_aux(const Params& p) {
 }
 // Read where it is used, for a block that the matrix ends in.
 template <int EPI>
-__device__ __forceinline__ void load_aux(const Params& p, int row0, int col, Aux& a) {
+__device__ __forceinline__ void load_aux(const Params& p, int row0, int col, int end, Aux& a) {
   using L = Lay<EPI>;
-  const int n = p.N - col;
+  const int n = end - col;
   if (!reads_aux<EPI>(p) || n <= 0) return;
 #pragma unroll
   for (int i = 0; i < L::NR; ++i) {
@@ -234,12 +235,12 @@ __device__ __forceinline__ void store_rows(T* out, int64_t ld, int row0, int M, 
 // FULL: the block lies inside the matrix, so that nothing is tested per element
 // and the rows' instructions interleave.
 template <int EPI, int ACT, bool FULL>
-__device__ __forceinline__ void linear_block(const Params& p, const DropKey& key, int row0, int col, int lane,
+__device__ __forceinline__ void linear_block(const Params& p, const DropKey& key, int row0, int col, int end, int lane,
                                              const float* st, const Aux& a) {
   using L = Lay<EPI>;
   using T = std::conditional_t<EPI == E_LINEAR_F32, float, bf16>;
   constexpr int NR = L::NR, NC = L::NC;
-  const int n = p.N - col;
+  const int n = end - col;
   if (!FULL && n <= 0) return;
   float v[NR][NC];
   staged_rows<EPI>(st, lane, v);
@@ -275,9 +276,9 @@ __device__ __forceinline__ void linear_block(const Params& p, const DropKey& key
 }
 
 template <int ACT, bool FULL>
-__device__ __forceinline__ void bwd_block(const Params& p, const DropKey& key, int row0, int col, int lane,
+__device__ __forceinline__ void bwd_block(const Params& p, const DropKey& key, int row0, int col, int end, int lane,
                                           const float* st, const Aux& a) {
-  const int n = p.N - col;
+  const int n = end - col;
   float v[4][8];
   staged_rows<E_BWD>(st, lane, v);
   if (ACT != MT_ACT_NONE) {
@@ -313,9 +314,9 @@ __device__ __forceinline__ void bwd_block(const Params& p, const DropKey& key, i
 }
 
 template <int ACT, bool FULL>
-__device__ __forceinline__ void gated_bwd_block(const Params& p, int row0, int col, int lane, const float* st,
-                                                const Aux& a) {
-  if (!FULL && col >= p.N) return;  // N is a multiple of 8
+__device__ __forceinline__ void gated_bwd_block(const Params& p, int row0, int col, int end, int lane,
+                                                const float* st, const Aux& a) {
+  if (!FULL && col >= end) return;  // end is a multiple of 8
   float v[4][8];
   staged_rows<E_GATED_BWD>(st, lane, v);
 #pragma unroll
@@ -342,28 +343,28 @@ __device__ __forceinline__ void gated_bwd_block(const Params& p, int row0, int c
 
 // One block with its activation and fullness as constants.
 template <int EPI>
-__device__ __forceinline__ void block(const Params& p, const DropKey& key, bool full, int row0, int col, int lane,
-                                      const float* st, const Aux& a) {
+__device__ __forceinline__ void block(const Params& p, const DropKey& key, bool full, int row0, int col, int end,
+                                      int lane, const float* st, const Aux& a) {
   if (full) {
-    if (EPI == E_LINEAR_BF16) MT_WITH_ACT(p.act, (linear_block<E_LINEAR_BF16, ACT, true>(p, key, row0, col, lane, st, a)));
-    if (EPI == E_LINEAR_F32) MT_WITH_ACT(p.act, (linear_block<E_LINEAR_F32, ACT, true>(p, key, row0, col, lane, st, a)));
-    if (EPI == E_BWD) MT_WITH_ACT(p.act, (bwd_block<ACT, true>(p, key, row0, col, lane, st, a)));
-    if (EPI == E_GATED_BWD) MT_WITH_ACT(p.act, (gated_bwd_block<ACT, true>(p, row0, col, lane, st, a)));
+    if (EPI == E_LINEAR_BF16) MT_WITH_ACT(p.act, (linear_block<E_LINEAR_BF16, ACT, true>(p, key, row0, col, end, lane, st, a)));
+    if (EPI == E_LINEAR_F32) MT_WITH_ACT(p.act, (linear_block<E_LINEAR_F32, ACT, true>(p, key, row0, col, end, lane, st, a)));
+    if (EPI == E_BWD) MT_WITH_ACT(p.act, (bwd_block<ACT, true>(p, key, row0, col, end, lane, st, a)));
+    if (EPI == E_GATED_BWD) MT_WITH_ACT(p.act, (gated_bwd_block<ACT, true>(p, row0, col, end, lane, st, a)));
   } else {
-    if (EPI == E_LINEAR_BF16) MT_WITH_ACT(p.act, (linear_block<E_LINEAR_BF16, ACT, false>(p, key, row0, col, lane, st, a)));
-    if (EPI == E_LINEAR_F32) MT_WITH_ACT(p.act, (linear_block<E_LINEAR_F32, ACT, false>(p, key, row0, col, lane, st, a)));
-    if (EPI == E_BWD) MT_WITH_ACT(p.act, (bwd_block<ACT, false>(p, key, row0, col, lane, st, a)));
-    if (EPI == E_GATED_BWD) MT_WITH_ACT(p.act, (gated_bwd_block<ACT, false>(p, row0, col, lane, st, a)));
+    if (EPI == E_LINEAR_BF16) MT_WITH_ACT(p.act, (linear_block<E_LINEAR_BF16, ACT, false>(p, key, row0, col, end, lane, st, a)));
+    if (EPI == E_LINEAR_F32) MT_WITH_ACT(p.act, (linear_block<E_LINEAR_F32, ACT, false>(p, key, row0, col, end, lane, st, a)));
+    if (EPI == E_BWD) MT_WITH_ACT(p.act, (bwd_block<ACT, false>(p, key, row0, col, end, lane, st, a)));
+    if (EPI == E_GATED_BWD) MT_WITH_ACT(p.act, (gated_bwd_block<ACT, false>(p, row0, col, end, lane, st, a)));
   }
 }
 
 // Gate and up meet in the registers of a row's lane; their bf16 blocks and h's
 // go through shared memory to be stored.
 template <int ACT>
-__device__ __forceinline__ void gated_block(const Params& p, int row0, int col, int lane, uint4* st,
+__device__ __forceinline__ void gated_block(const Params& p, int row0, int col, int end, int lane, uint4* st,
                                             const uint32_t (&a)[32], const uint32_t (&b)[32]) {
   float v[32];
-  const bool in = col < p.N;  // N is a multiple of 8
+  const bool in = col < end;  // end is a multiple of 8
   uint4* st2 = st + 128;      // the second half of the warp's buffer
   if (p.gu) {
 #pragma unroll
@@ -401,22 +402,25 @@ __device__ __forceinline__ void gated_block(const Params& p, int row0, int col, 
 // rows, the leader (rank 0) issues the MMAs, both CTAs' copies complete on the
 // leader's `full` barriers, the leader's commits release both CTAs' `empty`
 // stages and both `tfull` accumulators, and both CTAs' epilogue warps release
-// the leader's `tempty`. B_MN: B is stored [K, N]. tmB2 is Wu's map for a
-// gated product and unused otherwise.
+// the leader's `tempty`. tmB2 is Wu's map for a gated product and unused
+// otherwise.
 // ---------------------------------------------------------------------------
-template <int BN, bool PAIR, bool B_MN, int EPI>
-__global__ void __launch_bounds__(Cfg<BN, PAIR, EPI>::THREADS, 1)
+template <bool PAIR, int EPI>
+__global__ void __launch_bounds__(THREADS, 1)
     k_linear(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
              const __grid_constant__ CUtensorMap tmB2, const __grid_constant__ Params p) {
-  using C = Cfg<BN, PAIR, EPI>;
   constexpr bool GATED = EPI == E_GATED;
-  constexpr int ON = C::ON;
-  static_assert(!B_MN || BN >= 64, "an MN-major operand is staged 64 columns at a time");
+  constexpr bool B_MN = EPI == E_BWD || EPI == E_GATED_BWD;  // B is stored [K, N]
+  constexpr int TILE_M = PAIR ? 2 * BM : BM;
+  using F = Ahead<EPI>;
+  const int bn = p.t.bn, stages = p.t.stages;
+  const int on = GATED ? bn / 2 : bn;  // output columns of a tile
+  const uint32_t a_bytes = p.t.a_rows * (BK * 2), stage_bytes = a_bytes + p.t.b_rows * (BK * 2);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE_BYTES);
-  uint64_t* empty = full + C::STAGES;
-  uint64_t* tfull = empty + C::STAGES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + stages * stage_bytes);
+  uint64_t* empty = full + stages;
+  uint64_t* tfull = empty + stages;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -428,13 +432,13 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI>::THREADS, 1)
   const uint64_t limit = PAIR ? kWaitLimitNs : p.wait_ns;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::STAGES; ++s) {
+    for (int s = 0; s < stages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], C::EPI_WARPS * (PAIR ? 2 : 1));
+      mbar_init(&tempty[a], EPI_WARPS * (PAIR ? 2 : 1));
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -445,10 +449,10 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI>::THREADS, 1)
   }
   if (warp == 1) {
     if (PAIR) {
-      tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
+      tmem_alloc_pair(tmem_slot, TMEM_COLS);
       tmem_relinquish_pair();
     } else {
-      tmem_alloc(tmem_slot, C::TMEM_COLS);
+      tmem_alloc(tmem_slot, TMEM_COLS);
       tmem_relinquish();
     }
   }
@@ -460,8 +464,8 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
-  const int num_m = (p.M + C::TILE_M - 1) / C::TILE_M;
-  const int num_n = (p.N + ON - 1) / ON;
+  const int num_m = (p.M + TILE_M - 1) / TILE_M;
+  const int num_n = (p.N + on - 1) / on;
   const int num_tiles = num_m * num_n;
   const int num_kb = (p.K + BK - 1) / BK;
   const int first_tile = PAIR ? blockIdx.x >> 1 : blockIdx.x;
@@ -478,9 +482,9 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI>::THREADS, 1)
     for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
       int mb, nb;
       tile_coords(tile, num_m, num_n, mb, nb);
-      const int m0 = mb * C::TILE_M + (int)rank * BM;
+      const int m0 = mb * TILE_M + (int)rank * BM;
       // A pair's B rows are split over its CTAs; a gated tile has one half from each weight.
-      const int n0 = nb * ON + (PAIR && !GATED ? (int)rank * (BN / 2) : 0);
+      const int n0 = nb * on + (PAIR && !GATED ? (int)rank * (bn / 2) : 0);
       const CUtensorMap* mB = PAIR && GATED && rank ? &tmB2 : &tmB;
       for (int kb = 0; kb < num_kb; ++kb) {
         const bool got = mbar_wait_u32(empty0 + 8 * stage, phase ^ 1, limit);
@@ -488,36 +492,34 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI>::THREADS, 1)
           ok = false;
           break;
         }
-        uint8_t* sa = smem + stage * C::STAGE_BYTES;
-        uint8_t* sb = sa + C::A_BYTES;
+        uint8_t* sa = smem + stage * stage_bytes;
+        uint8_t* sb = sa + a_bytes;
         const int k0 = kb * BK;
         if (elect_one()) {
           if (PAIR) {
             const uint32_t fb = fb0 + 8 * stage;
-            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::STAGE_BYTES);
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * stage_bytes);
             tma_load_2d_pair(sa, &tmA, fb, k0, m0);
             if (!B_MN) {
               tma_load_2d_pair(sb, mB, fb, k0, n0);
             } else {
-#pragma unroll
-              for (int i = 0; i < C::B_ROWS / 64; ++i) tma_load_2d_pair(sb + i * 8192, mB, fb, n0 + i * 64, k0);
+              for (int i = 0; i < p.t.b_rows / 64; ++i) tma_load_2d_pair(sb + i * 8192, mB, fb, n0 + i * 64, k0);
             }
           } else {
-            mbar_arrive_expect_tx(&full[stage], C::STAGE_BYTES);
+            mbar_arrive_expect_tx(&full[stage], stage_bytes);
             tma_load_2d(sa, &tmA, &full[stage], k0, m0);
             if (GATED) {
               tma_load_2d(sb, &tmB, &full[stage], k0, n0);
-              tma_load_2d(sb + C::B_BYTES / 2, &tmB2, &full[stage], k0, n0);
+              tma_load_2d(sb + (stage_bytes - a_bytes) / 2, &tmB2, &full[stage], k0, n0);
             } else if (!B_MN) {
               tma_load_2d(sb, &tmB, &full[stage], k0, n0);
             } else {
-#pragma unroll
-              for (int i = 0; i < C::B_ROWS / 64; ++i) tma_load_2d(sb + i * 8192, &tmB, &full[stage], n0 + i * 64, k0);
+              for (int i = 0; i < p.t.b_rows / 64; ++i) tma_load_2d(sb + i * 8192, &tmB, &full[stage], n0 + i * 64, k0);
             }
           }
         }
         ++issued;
-        if (++stage == C::STAGES) {
+        if (++stage == stages) {
           stage = 0;
           phase ^= 1;
         }
@@ -533,7 +535,7 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI>::THREADS, 1)
         // Wait until the MMA has released every stage, so that no commit is on
         // its way to this CTA's barriers when it exits. If another role gives
         // up meanwhile, the MMA may never release them: drain the copies below.
-        for (int i = 0; i < C::STAGES && ok; ++i) {
+        for (int i = 0; i < stages && ok; ++i) {
           const uint64_t t0 = globaltimer();
           while (!mbar_wait(&empty[stage], phase ^ 1, 0)) {
             if (!PAIR && *abort_flag) {
@@ -547,7 +549,7 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI>::THREADS, 1)
               break;
             }
           }
-          if (++stage == C::STAGES) {
+          if (++stage == stages) {
             stage = 0;
             phase ^= 1;
           }
@@ -557,8 +559,8 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI>::THREADS, 1)
         // Every issued copy lands before the shared memory goes away: stage s
         // was last filled by fill s + STAGES q (the largest below `issued`), in
         // phase q mod 2. The leader's barriers count both CTAs' bytes.
-        for (int s = 0; s < C::STAGES && s < issued; ++s) {
-          const int q = (issued - 1 - s) / C::STAGES;
+        for (int s = 0; s < stages && s < issued; ++s) {
+          const int q = (issued - 1 - s) / stages;
           if (!mbar_wait(&full[s], (uint32_t)(q & 1))) record_error(p.err, DEV_TIMEOUT_TEARDOWN);
         }
       }
@@ -571,12 +573,12 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI>::THREADS, 1)
       // loop inside one lane's branch, every MMA and commit first moved its
       // operands to uniform registers, and a k-block took 560 cycles and more
       // to issue where the tensor core needs 512.
-      constexpr uint32_t idesc = idesc_bf16_f32(C::TILE_M, BN, false, B_MN);
+      const uint32_t idesc = idesc_bf16_f32(TILE_M, bn, false, B_MN);
       // Descriptors of stage 0; stages and k-steps only move the start address.
       const uint32_t s0 = smem_u32(smem);
       const uint64_t a0 = sdesc_sw128(s0, 16, 1024);
-      const uint64_t b0 = sdesc_sw128(s0 + C::A_BYTES, B_MN ? 8192 : 16, 1024);
-      constexpr uint32_t kStage = C::STAGE_BYTES >> 4;
+      const uint64_t b0 = sdesc_sw128(s0 + a_bytes, B_MN ? 8192 : 16, 1024);
+      const uint32_t kStage = stage_bytes >> 4;
       constexpr uint32_t kAStep = 32 >> 4, kBStep = (B_MN ? 2048 : 32) >> 4;
       const uint32_t full0 = smem_u32(&full[0]), empty0 = smem_u32(&empty[0]), tfull0 = smem_u32(&tfull[0]);
       int stage = 0;
@@ -593,7 +595,7 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI>::THREADS, 1)
           break;
         }
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + acc * BN;
+        const uint32_t d_tmem = tmem_base + acc * 256;
         for (int kb = 0; kb < num_kb; ++kb) {
           if (!__all_sync(0xffffffffu, mbar_wait_u32(full0 + 8 * stage, phase, limit))) {
             ok = false;
@@ -622,7 +624,7 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI>::THREADS, 1)
             }
           }
           issued = true;
-          if (++stage == C::STAGES) {
+          if (++stage == stages) {
             stage = 0;
             phase ^= 1;
           }
@@ -653,30 +655,30 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI>::THREADS, 1)
   } else {
     // ---------------- epilogue ----------------
     const int quarter = warp & 3;                // tensor-memory lanes this warp may read
-    const int share = ((warp - 2) >> 2) * C::OW;
-    uint8_t* mine = smem + C::STAGES * C::STAGE_BYTES + 256;
+    const int half = (warp - 2) >> 2;  // takes blocks half, half + 2, ...
+    uint8_t* mine = smem + stages * stage_bytes + BAR_BYTES;
     float* st = reinterpret_cast<float*>(mine + (warp - 2) * EPI_BYTES);
-    const uint4* fetched = reinterpret_cast<uint4*>(mine + C::EPI_WARPS * EPI_BYTES + (warp - 2) * C::DEPTH * C::AUX_BLOCK) + lane;
+    const uint4* fetched = reinterpret_cast<uint4*>(mine + EPI_WARPS * EPI_BYTES + (warp - 2) * F::DEPTH * F::BLOCK) + lane;
     const DropKey key = drop_key(p.drop);
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int tile = first_tile; tile < num_tiles; tile += tile_step) {
       int mb, nb;
       tile_coords(tile, num_m, num_n, mb, nb);
-      const int row0 = mb * C::TILE_M + (int)rank * BM + quarter * 32 + Lay<EPI>::row(lane);  // this lane's first row
-      const int col0 = nb * ON + share;
-      const int blocks = min(C::OW, p.N - col0 + 31) >> 5;  // none (or less) where the share lies behind the last column
-      const bool full_rows = mb * C::TILE_M + (int)rank * BM + quarter * 32 + 32 <= p.M;
-      auto inside = [&](int k) { return full_rows && col0 + 32 * k + 32 <= p.N; };
+      const int row0 = mb * TILE_M + (int)rank * BM + quarter * 32 + Lay<EPI>::row(lane);  // this lane's first row
+      const int col0 = nb * on + 32 * half, end = min(p.N, (nb + 1) * on);
+      const int blocks = (end - col0 + 63) >> 6;  // none (or less) where the tile has no block for this warp
+      const bool full_rows = mb * TILE_M + (int)rank * BM + quarter * 32 + 32 <= p.M;
+      auto inside = [&](int k) { return full_rows && col0 + 64 * k + 32 <= end; };
       // One group of copies to a block, empty where there is nothing to copy.
       auto fetch = [&](int k) {
-        if (C::AUX_BLOCK == 0) return;
+        if (F::BLOCK == 0) return;
         if (k < blocks && inside(k))
-          fetch_aux<EPI>(p, smem_u32(fetched) + k % C::DEPTH * C::AUX_BLOCK, row0, col0 + 32 * k + Lay<EPI>::col(lane));
+          fetch_aux<EPI>(p, smem_u32(fetched) + k % F::DEPTH * F::BLOCK, row0, col0 + 64 * k + Lay<EPI>::col(lane));
         copy_commit();
       };
 #pragma unroll
-      for (int k = 0; k < C::DEPTH; ++k) fetch(k);  // while the main loop runs
+      for (int k = 0; k < F::DEPTH; ++k) fetch(k);  // while the main loop runs
       // warp-uniform outcome: the tcgen05.ld below is warp-collective
       if (__any_sync(0xffffffffu, *abort_flag) ||
           !__all_sync(0xffffffffu, mbar_wait(&tfull[acc], acc_phase, limit))) {
@@ -685,7 +687,7 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI>::THREADS, 1)
         break;
       }
       tc_fence_after();
-      const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * BN + share;
+      const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * 256 + 32 * half;
       // Hands the accumulator back as soon as its last columns are in registers.
       auto release = [&] {
         tc_fence_before();
@@ -700,30 +702,30 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI>::THREADS, 1)
       if (blocks <= 0) release();
 #pragma unroll 1
       for (int k = 0; k < blocks; ++k) {
-        const int col = col0 + 32 * k + Lay<EPI>::col(lane);  // this lane's first column
+        const int col = col0 + 64 * k + Lay<EPI>::col(lane);  // this lane's first column
         uint32_t a[32];
-        tmem_ld_32x32b_x32(tbase + 32 * k, a);
+        tmem_ld_32x32b_x32(tbase + 64 * k, a);
         if (GATED) {
           uint32_t b[32];
-          tmem_ld_32x32b_x32(tbase + BN / 2 + 32 * k, b);
+          tmem_ld_32x32b_x32(tbase + on + 64 * k, b);
           tmem_ld_wait();
           if (k == blocks - 1) release();
-          MT_WITH_ACT(p.act, (gated_block<ACT>(p, row0, col, lane, reinterpret_cast<uint4*>(st), a, b)));
+          MT_WITH_ACT(p.act, (gated_block<ACT>(p, row0, col, end, lane, reinterpret_cast<uint4*>(st), a, b)));
         } else {
           tmem_ld_wait();
           if (k == blocks - 1) release();
           stage_f32(st, lane, a);
           __syncwarp();
           Aux aux;
-          if (C::AUX_BLOCK > 0) {
-            copy_wait<C::DEPTH - 1>();
+          if (reads_aux<EPI>(p)) {  // its slots exist only then
+            copy_wait<F::DEPTH - 1>();
             if (inside(k))
-              fetched_aux<EPI>(fetched + k % C::DEPTH * (C::AUX_BLOCK / 16), aux);
+              fetched_aux<EPI>(fetched + k % F::DEPTH * (F::BLOCK / 16), aux);
             else
-              load_aux<EPI>(p, row0, col, aux);
+              load_aux<EPI>(p, row0, col, end, aux);
           }
-          block<EPI>(p, key, inside(k), row0, col, lane, st, aux);
-          fetch(k + C::DEPTH);
+          block<EPI>(p, key, inside(k), row0, col, end, lane, st, aux);
+          fetch(k + F::DEPTH);
         }
         __syncwarp();  // the buffer is free for the next block
       }
@@ -744,9 +746,9 @@ __global__ void __launch_bounds__(Cfg<BN, PAIR, EPI>::THREADS, 1)
   if (warp == 1) {
     tc_fence_after();
     if (PAIR)
-      tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+      tmem_dealloc_pair(tmem_base, TMEM_COLS);
     else
-      tmem_dealloc(tmem_base, C::TMEM_COLS);
+      tmem_dealloc(tmem_base, TMEM_COLS);
   }
 }
 
@@ -765,16 +767,30 @@ struct Op {
   Params p;
 };
 
-template <int BN, bool PAIR, bool B_MN, int EPI>
-int launch(const Op& o, int device, int num_sms, cudaStream_t st) {
-  using C = Cfg<BN, PAIR, EPI>;
-  constexpr bool GATED = EPI == E_GATED;
-  constexpr int ON = C::ON;
-  auto kernel = k_linear<BN, PAIR, B_MN, EPI>;
-  const Params& p = o.p;
+template <bool PAIR, int EPI>
+int launch(Op o, int bn, int device, int num_sms, cudaStream_t st) {
+  constexpr bool GATED = EPI == E_GATED, B_MN = EPI == E_BWD || EPI == E_GATED_BWD;
+  constexpr int TILE_M = PAIR ? 2 * BM : BM;
+  auto kernel = k_linear<PAIR, EPI>;
+  Params& p = o.p;
+  // Rows of A behind the last are not staged: an MMA then reads what lies
+  // behind them in shared memory, and only its rows that are not stored see it.
+  const int on = GATED ? bn / 2 : bn;
+  p.t.bn = bn;
+  p.t.a_rows = PAIR || p.M >= BM ? BM : (p.M + 7) / 8 * 8;
+  p.t.b_rows = PAIR ? bn / 2 : bn;
+  const bool aux = EPI == E_BWD ? p.act != MT_ACT_NONE : EPI == E_GATED_BWD ? true : EPI != E_GATED && p.R;
+  const int epi = EPI_WARPS * (EPI_BYTES + (aux ? Ahead<EPI>::DEPTH * Ahead<EPI>::BLOCK : 0));
+  const int stage = (p.t.a_rows + p.t.b_rows) * BK * 2;
+  const int fit = (SMEM_MOST - 1024 - BAR_BYTES - epi) / stage;
+  p.t.stages = fit < MAX_STAGES ? fit : MAX_STAGES;
+  // An MMA on fewer staged rows of A still reads 16 KB from the stage's start.
+  const int used = p.t.stages * stage + BAR_BYTES + epi;
+  const int smem = 1024 + (used > (p.t.stages - 1) * stage + BM * BK * 2 ? used : (p.t.stages - 1) * stage + BM * BK * 2);
+
   CUtensorMap ta, tb, tb2;
-  bool ok = make_tensor_map_2d_bf16(&ta, o.A, p.K, p.M, o.lda, BM);
-  const int b_box = GATED && !PAIR ? C::B_ROWS / 2 : C::B_ROWS;
+  bool ok = make_tensor_map_2d_bf16(&ta, o.A, p.K, p.M, o.lda, p.t.a_rows);
+  const int b_box = GATED && !PAIR ? bn / 2 : p.t.b_rows;
   ok = ok && (B_MN ? make_tensor_map_2d_bf16(&tb, o.B, p.N, p.K, o.ldb, 64)
                    : make_tensor_map_2d_bf16(&tb, o.B, p.K, p.N, o.ldb, b_box));
   tb2 = tb;
@@ -782,8 +798,8 @@ int launch(const Op& o, int device, int num_sms, cudaStream_t st) {
   if (!ok) return MT_ERR_ARG;
 
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(C::THREADS, 1, 1);
-  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -798,7 +814,7 @@ int launch(const Op& o, int device, int num_sms, cudaStream_t st) {
   // resident together. Threads that race here write the same value.
   static int resident[kMaxDevices] = {};
   if (resident[device] == 0) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MOST) != cudaSuccess)
       return MT_ERR_CUDA;
     int r = PAIR ? num_sms / 2 : num_sms;
     if (PAIR) {
@@ -811,7 +827,7 @@ int launch(const Op& o, int device, int num_sms, cudaStream_t st) {
     }
     resident[device] = r;
   }
-  const int64_t tiles = (int64_t)((p.M + C::TILE_M - 1) / C::TILE_M) * ((p.N + ON - 1) / ON);
+  const int64_t tiles = (int64_t)((p.M + TILE_M - 1) / TILE_M) * ((p.N + on - 1) / on);
   if (tiles > INT32_MAX / 2) return MT_ERR_ARG;
   const int n = tiles < resident[device] ? (int)tiles : resident[device];
   cfg.gridDim = dim3(PAIR ? 2 * n : n, 1, 1);
@@ -819,17 +835,11 @@ int launch(const Op& o, int device, int num_sms, cudaStream_t st) {
   return launch_status();
 }
 
-// Tiles dealt to `n` resident CTAs or pairs, in whole waves.
-int64_t waves(int64_t M, int64_t N, int tm, int tn, int n) {
-  const int64_t tiles = ((M + tm - 1) / tm) * ((N + tn - 1) / tn);
-  return (tiles + n - 1) / n;
-}
-
-// The tile is the one whose waves cost least, where a k-block of a 128 x BN
-// tile is taken to cost BN + 32 (its columns on the tensor core, and a fixed
-// part for staging A and for the waits) and a pair's 256-row tile to cost as
-// much as one CTA's 128 rows.
-template <bool B_MN, int EPI>
+// The tile is the one whose waves cost least. A k-block costs an SM the larger
+// of its MMAs (2 bn cycles for 128 rows, or for each half of a pair's 256) and
+// of fetching its operands from L2 at about 60 bytes a cycle, which is what
+// bounds narrow tiles: 128 x 128 takes 546 cycles for 256 of MMA.
+template <int EPI>
 int dispatch(const Op& o, cudaStream_t st) {
   int device = 0, sms = 0;
   if (cudaGetDevice(&device) != cudaSuccess || device >= kMaxDevices) return MT_ERR_CUDA;
@@ -840,35 +850,26 @@ int dispatch(const Op& o, cudaStream_t st) {
     num_sms[device] = sms;
   }
   sms = num_sms[device];
+  constexpr bool B_MN = EPI == E_BWD || EPI == E_GATED_BWD;
   constexpr int G = EPI == E_GATED ? 2 : 1;  // a gated tile spends half of its columns on each of gate and up
   const int family = gemm_variant_now();
   int best = 0;
-  int64_t cost = INT64_MAX;
-  auto consider = [&](int id, int bn, bool pair) {
-    const int64_t w = waves(o.p.M, o.p.N, pair ? 2 * BM : BM, bn / G, pair ? sms / 2 : sms);
-    const int64_t c = w * (bn + 32);
-    if (c < cost) cost = c, best = id;
+  bool best_pair = false;
+  int64_t least = INT64_MAX;
+  auto consider = [&](int bn, bool pair) {
+    const int tm = pair ? 2 * BM : BM, tn = bn / G, n = pair ? sms / 2 : sms;
+    const int64_t tiles = ((int64_t)o.p.M + tm - 1) / tm * ((o.p.N + tn - 1) / tn);
+    const int bytes = (o.p.M < BM ? o.p.M : BM) * 128 + (pair ? bn / 2 : bn) * 128;
+    const int64_t cost = (tiles + n - 1) / n * (2 * bn * 60 > bytes ? 2 * bn * 60 : bytes);
+    if (cost < least) least = cost, best = bn, best_pair = pair;
   };
-  if (family != 1) consider(0, 256, true);
-  if (family != 1) consider(1, 128, true);
-  if (family != 2) {
-    if (G == 2) consider(2, 256, false);
-    consider(3, 128, false);
-    consider(4, 64, false);
-    if (!B_MN && G == 1) consider(5, 32, false);
-  }
-  switch (best) {
-    case 0: return launch<256, true, B_MN, EPI>(o, device, sms, st);
-    case 1: return launch<128, true, B_MN, EPI>(o, device, sms, st);
-    case 3: return launch<128, false, B_MN, EPI>(o, device, sms, st);
-    case 4: return launch<64, false, B_MN, EPI>(o, device, sms, st);
-    case 5:
-      if constexpr (!B_MN && G == 1) return launch<32, false, B_MN, EPI>(o, device, sms, st);
-      break;
-    default:
-      if constexpr (G == 2) return launch<256, false, B_MN, EPI>(o, device, sms, st);
-  }
-  return MT_ERR_CONFIG;  // not reached
+  // MN-major operands are staged 64 columns at a time; MMAs take widths of
+  // multiples of 16 (a pair's of 32).
+  if (family != 1)
+    for (int bn = 256; bn >= (B_MN ? 128 : 64); bn -= B_MN ? 128 : 32) consider(bn, true);
+  if (family != 2)
+    for (int bn = 256; bn >= (B_MN ? 64 : 32); bn -= B_MN ? 64 : 16) consider(bn, false);
+  return best_pair ? launch<true, EPI>(o, best, device, sms, st) : launch<false, EPI>(o, best, device, sms, st);
 }
 
 }  // namespace
@@ -880,7 +881,7 @@ int launch_linear_fwd(const LinearFwd& a, const DropDesc& drop, cudaStream_t st,
   p.M = a.M, p.N = a.N, p.K = a.K, p.act = a.act, p.drop = drop;
   p.bias = (const bf16*)a.bias, p.R = a.R, p.ldr = a.ldr, p.Z = (bf16*)a.Z, p.ldz = a.ldz, p.C = a.C, p.ldc = a.ldc;
   p.err = dev_err, p.wait_ns = gemm_wait_limit_now();
-  return a.out_type == MT_F32 ? dispatch<false, E_LINEAR_F32>(o, st) : dispatch<false, E_LINEAR_BF16>(o, st);
+  return a.out_type == MT_F32 ? dispatch<E_LINEAR_F32>(o, st) : dispatch<E_LINEAR_BF16>(o, st);
 }
 
 size_t linear_bwd_partial_floats(int M, int N) { return (size_t)((M + 31) / 32) * ((N + 3) & ~3); }
@@ -892,7 +893,7 @@ int launch_linear_bwd_act(const LinearBwd& a, const DropDesc& drop, cudaStream_t
   p.M = a.M, p.N = a.N, p.K = a.K, p.act = a.act, p.drop = drop;
   p.Z = (bf16*)a.Z, p.ldz = a.ldz, p.C = a.dZ, p.ldc = a.lddz, p.part = a.db ? a.part : nullptr;
   p.err = dev_err, p.wait_ns = gemm_wait_limit_now();
-  if (const int rc = dispatch<true, E_BWD>(o, st)) return rc;
+  if (const int rc = dispatch<E_BWD>(o, st)) return rc;
   return a.db ? launch_column_sums(a.part, (a.M + 31) / 32, (a.N + 3) & ~3, a.N, a.db, a.N, nullptr, st) : MT_OK;
 }
 
@@ -903,7 +904,7 @@ int launch_gated_ffn_fwd(const void* x, int64_t ldx, const void* Wgu, int64_t ld
   Params& p = o.p;
   p.M = M, p.N = F, p.K = K, p.act = act, p.gu = (bf16*)gu, p.ldgu = ldgu, p.C = h, p.ldc = ldh;
   p.err = dev_err, p.wait_ns = gemm_wait_limit_now();
-  return dispatch<false, E_GATED>(o, st);
+  return dispatch<E_GATED>(o, st);
 }
 
 int launch_gated_ffn_bwd(const void* dy, int64_t lddy, const void* Wd, int64_t ldw, const void* gu, int64_t ldgu,
@@ -914,7 +915,7 @@ int launch_gated_ffn_bwd(const void* dy, int64_t lddy, const void* Wd, int64_t l
   Params& p = o.p;
   p.M = M, p.N = F, p.K = K, p.act = act, p.gu = (bf16*)gu, p.ldgu = ldgu, p.dgu = (bf16*)dgu, p.lddgu = lddgu;
   p.C = h, p.ldc = ldh, p.err = dev_err, p.wait_ns = gemm_wait_limit_now();
-  return dispatch<true, E_GATED_BWD>(o, st);
+  return dispatch<E_GATED_BWD>(o, st);
 }
 
 }  // namespace mt
