@@ -54,10 +54,12 @@ struct Ahead {
 };
 
 // The tile and the pipeline of a launch, chosen by the host. A tile is 128
-// rows (256 for a pair of CTAs) by bn columns; a stage holds a_rows rows of A
-// and b_rows of B, 64 deep.
+// rows (256 for a pair of CTAs) by bn columns. A stage holds `sub` k-blocks of
+// a_rows rows of A and b_rows of B, 64 deep: several where they are small, so
+// that a barrier is passed for 16 KB or more and rows are read 128 sub bytes at
+// a time.
 struct Tile {
-  int bn, a_rows, b_rows, stages;
+  int bn, a_rows, b_rows, sub, stages;
 };
 
 struct Params {
@@ -415,7 +417,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   using F = Ahead<EPI>;
   const int bn = p.t.bn, stages = p.t.stages;
   const int on = GATED ? bn / 2 : bn;  // output columns of a tile
-  const uint32_t a_bytes = p.t.a_rows * (BK * 2), stage_bytes = a_bytes + p.t.b_rows * (BK * 2);
+  const uint32_t a_bytes = p.t.a_rows * (BK * 2), kb_bytes = a_bytes + p.t.b_rows * (BK * 2);
+  const int sub = p.t.sub;
+  const uint32_t stage_bytes = sub * kb_bytes;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + stages * stage_bytes);
@@ -486,36 +490,47 @@ __global__ void __launch_bounds__(THREADS, 1)
       // A pair's B rows are split over its CTAs; a gated tile has one half from each weight.
       const int n0 = nb * on + (PAIR && !GATED ? (int)rank * (bn / 2) : 0);
       const CUtensorMap* mB = PAIR && GATED && rank ? &tmB2 : &tmB;
-      for (int kb = 0; kb < num_kb; ++kb) {
+      for (int kb = 0; kb < num_kb; kb += sub) {
         const bool got = mbar_wait_u32(empty0 + 8 * stage, phase ^ 1, limit);
         if (!__all_sync(0xffffffffu, got && !*abort_flag)) {
           ok = false;
           break;
         }
         uint8_t* sa = smem + stage * stage_bytes;
-        uint8_t* sb = sa + a_bytes;
-        const int k0 = kb * BK;
+        const int n = min(sub, num_kb - kb);  // k-blocks of this stage
+        int k0 = kb * BK;
         if (elect_one()) {
-          if (PAIR) {
-            const uint32_t fb = fb0 + 8 * stage;
-            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * stage_bytes);
-            tma_load_2d_pair(sa, &tmA, fb, k0, m0);
-            if (!B_MN) {
-              tma_load_2d_pair(sb, mB, fb, k0, n0);
+          const uint32_t fb = fb0 + 8 * stage;
+          if (!PAIR || rank == 0) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * n * kb_bytes);
+          auto load = [&] {
+            uint8_t* sb = sa + a_bytes;
+            if (PAIR) {
+              tma_load_2d_pair(sa, &tmA, fb, k0, m0);
+              if (!B_MN) {
+                tma_load_2d_pair(sb, mB, fb, k0, n0);
+              } else {
+                tma_load_2d_pair(sb, mB, fb, n0, k0);
+                if (p.t.b_rows > 64) tma_load_2d_pair(sb + 8192, mB, fb, n0 + 64, k0);
+              }
             } else {
-              for (int i = 0; i < p.t.b_rows / 64; ++i) tma_load_2d_pair(sb + i * 8192, mB, fb, n0 + i * 64, k0);
+              tma_load_2d(sa, &tmA, &full[stage], k0, m0);
+              if (GATED) {
+                tma_load_2d(sb, &tmB, &full[stage], k0, n0);
+                tma_load_2d(sb + (kb_bytes - a_bytes) / 2, &tmB2, &full[stage], k0, n0);
+              } else if (!B_MN) {
+                tma_load_2d(sb, &tmB, &full[stage], k0, n0);
+              } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                  if (c * 64 < p.t.b_rows) tma_load_2d(sb + c * 8192, &tmB, &full[stage], n0 + c * 64, k0);
+              }
             }
-          } else {
-            mbar_arrive_expect_tx(&full[stage], stage_bytes);
-            tma_load_2d(sa, &tmA, &full[stage], k0, m0);
-            if (GATED) {
-              tma_load_2d(sb, &tmB, &full[stage], k0, n0);
-              tma_load_2d(sb + (stage_bytes - a_bytes) / 2, &tmB2, &full[stage], k0, n0);
-            } else if (!B_MN) {
-              tma_load_2d(sb, &tmB, &full[stage], k0, n0);
-            } else {
-              for (int i = 0; i < p.t.b_rows / 64; ++i) tma_load_2d(sb + i * 8192, &tmB, &full[stage], n0 + i * 64, k0);
-            }
+          };
+          load();
+#pragma unroll 1
+          for (int i = 1; i < n; ++i) {
+            sa += kb_bytes, k0 += BK;
+            load();
           }
         }
         ++issued;
@@ -578,7 +593,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint32_t s0 = smem_u32(smem);
       const uint64_t a0 = sdesc_sw128(s0, 16, 1024);
       const uint64_t b0 = sdesc_sw128(s0 + a_bytes, B_MN ? 8192 : 16, 1024);
-      const uint32_t kStage = stage_bytes >> 4;
+      const uint32_t kStage = stage_bytes >> 4, kBlock = kb_bytes >> 4;
       constexpr uint32_t kAStep = 32 >> 4, kBStep = (B_MN ? 2048 : 32) >> 4;
       const uint32_t full0 = smem_u32(&full[0]), empty0 = smem_u32(&empty[0]), tfull0 = smem_u32(&tfull[0]);
       int stage = 0;
@@ -596,27 +611,36 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * 256;
-        for (int kb = 0; kb < num_kb; ++kb) {
+        for (int kb = 0; kb < num_kb; kb += sub) {
           if (!__all_sync(0xffffffffu, mbar_wait_u32(full0 + 8 * stage, phase, limit))) {
             ok = false;
             break;
           }
           // The stage's bytes were written by TMA and published through this
           // mbarrier, which orders them for the MMAs' reads: no tcgen05 fence.
-          const uint64_t ad = a0 + stage * kStage, bd = b0 + stage * kStage;
+          uint64_t ad = a0 + stage * kStage, bd = b0 + stage * kStage;
+          const int n = min(sub, num_kb - kb);
           if (elect_one()) {
+            auto multiply = [&](bool accumulate) {
 #pragma unroll
-            for (int kk = 0; kk < BK / 16; ++kk) {
-              if (PAIR)
-                umma_bf16_pair(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, (kb | kk) != 0);
-              else
-                umma_bf16(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, (kb | kk) != 0);
+              for (int kk = 0; kk < BK / 16; ++kk) {
+                if (PAIR)
+                  umma_bf16_pair(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, accumulate || kk != 0);
+                else
+                  umma_bf16(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, accumulate || kk != 0);
+              }
+            };
+            multiply(kb != 0);
+#pragma unroll 1
+            for (int i = 1; i < n; ++i) {
+              ad += kBlock, bd += kBlock;
+              multiply(true);
             }
             if (PAIR)
               umma_commit_both(empty0 + 8 * stage);
             else
               umma_commit_u32(empty0 + 8 * stage);
-            if (kb == num_kb - 1) {
+            if (kb + n == num_kb) {
               if (PAIR)
                 umma_commit_both(tfull0 + 8 * acc);
               else
@@ -655,7 +679,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else {
     // ---------------- epilogue ----------------
     const int quarter = warp & 3;                // tensor-memory lanes this warp may read
-    const int half = (warp - 2) >> 2;  // takes blocks half, half + 2, ...
+    const int half = (warp - 2) >> 2;            // takes the first or the second half of the tile's blocks
     uint8_t* mine = smem + stages * stage_bytes + BAR_BYTES;
     float* st = reinterpret_cast<float*>(mine + (warp - 2) * EPI_BYTES);
     const uint4* fetched = reinterpret_cast<uint4*>(mine + EPI_WARPS * EPI_BYTES + (warp - 2) * F::DEPTH * F::BLOCK) + lane;
@@ -666,15 +690,16 @@ __global__ void __launch_bounds__(THREADS, 1)
       int mb, nb;
       tile_coords(tile, num_m, num_n, mb, nb);
       const int row0 = mb * TILE_M + (int)rank * BM + quarter * 32 + Lay<EPI>::row(lane);  // this lane's first row
-      const int col0 = nb * on + 32 * half, end = min(p.N, (nb + 1) * on);
-      const int blocks = (end - col0 + 63) >> 6;  // none (or less) where the tile has no block for this warp
+      const int end = min(p.N, (nb + 1) * on), all = (end - nb * on + 31) >> 5, first_half = (all + 1) >> 1;
+      const int blocks = half ? all - first_half : first_half;  // 0 in the second half of a tile of one block
+      const int share = half ? 32 * first_half : 0, col0 = nb * on + share;
       const bool full_rows = mb * TILE_M + (int)rank * BM + quarter * 32 + 32 <= p.M;
-      auto inside = [&](int k) { return full_rows && col0 + 64 * k + 32 <= end; };
+      auto inside = [&](int k) { return full_rows && col0 + 32 * k + 32 <= end; };
       // One group of copies to a block, empty where there is nothing to copy.
       auto fetch = [&](int k) {
         if (F::BLOCK == 0) return;
         if (k < blocks && inside(k))
-          fetch_aux<EPI>(p, smem_u32(fetched) + k % F::DEPTH * F::BLOCK, row0, col0 + 64 * k + Lay<EPI>::col(lane));
+          fetch_aux<EPI>(p, smem_u32(fetched) + k % F::DEPTH * F::BLOCK, row0, col0 + 32 * k + Lay<EPI>::col(lane));
         copy_commit();
       };
 #pragma unroll
@@ -687,7 +712,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         break;
       }
       tc_fence_after();
-      const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * 256 + 32 * half;
+      const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * 256 + share;
       // Hands the accumulator back as soon as its last columns are in registers.
       auto release = [&] {
         tc_fence_before();
@@ -699,15 +724,15 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_arrive(&tempty[acc]);
         }
       };
-      if (blocks <= 0) release();
+      if (blocks == 0) release();
 #pragma unroll 1
       for (int k = 0; k < blocks; ++k) {
-        const int col = col0 + 64 * k + Lay<EPI>::col(lane);  // this lane's first column
+        const int col = col0 + 32 * k + Lay<EPI>::col(lane);  // this lane's first column
         uint32_t a[32];
-        tmem_ld_32x32b_x32(tbase + 64 * k, a);
+        tmem_ld_32x32b_x32(tbase + 32 * k, a);
         if (GATED) {
           uint32_t b[32];
-          tmem_ld_32x32b_x32(tbase + on + 64 * k, b);
+          tmem_ld_32x32b_x32(tbase + on + 32 * k, b);
           tmem_ld_wait();
           if (k == blocks - 1) release();
           MT_WITH_ACT(p.act, (gated_block<ACT>(p, row0, col, end, lane, reinterpret_cast<uint4*>(st), a, b)));
@@ -781,12 +806,16 @@ int launch(Op o, int bn, int device, int num_sms, cudaStream_t st) {
   p.t.b_rows = PAIR ? bn / 2 : bn;
   const bool aux = EPI == E_BWD ? p.act != MT_ACT_NONE : EPI == E_GATED_BWD ? true : EPI != E_GATED && p.R;
   const int epi = EPI_WARPS * (EPI_BYTES + (aux ? Ahead<EPI>::DEPTH * Ahead<EPI>::BLOCK : 0));
-  const int stage = (p.t.a_rows + p.t.b_rows) * BK * 2;
+  const int kb_bytes = (p.t.a_rows + p.t.b_rows) * BK * 2;
+  const int num_kb = (p.K + BK - 1) / BK;
+  p.t.sub = kb_bytes > 16384 ? 1 : kb_bytes > 8192 ? 2 : 4;
+  if (p.t.sub > num_kb) p.t.sub = num_kb;
+  const int stage = p.t.sub * kb_bytes;
   const int fit = (SMEM_MOST - 1024 - BAR_BYTES - epi) / stage;
   p.t.stages = fit < MAX_STAGES ? fit : MAX_STAGES;
   // An MMA on fewer staged rows of A still reads 16 KB from the stage's start.
-  const int used = p.t.stages * stage + BAR_BYTES + epi;
-  const int smem = 1024 + (used > (p.t.stages - 1) * stage + BM * BK * 2 ? used : (p.t.stages - 1) * stage + BM * BK * 2);
+  const int used = p.t.stages * stage + BAR_BYTES + epi, read = p.t.stages * stage - kb_bytes + BM * BK * 2;
+  const int smem = 1024 + (used > read ? used : read);
 
   CUtensorMap ta, tb, tb2;
   bool ok = make_tensor_map_2d_bf16(&ta, o.A, p.K, p.M, o.lda, p.t.a_rows);
@@ -861,7 +890,8 @@ int dispatch(const Op& o, cudaStream_t st) {
     const int64_t tiles = ((int64_t)o.p.M + tm - 1) / tm * ((o.p.N + tn - 1) / tn);
     const int bytes = (o.p.M < BM ? o.p.M : BM) * 128 + (pair ? bn / 2 : bn) * 128;
     const int64_t cost = (tiles + n - 1) / n * (2 * bn * 60 > bytes ? 2 * bn * 60 : bytes);
-    if (cost < least) least = cost, best = bn, best_pair = pair;
+    // On a tie the wider tile, but single CTAs before pairs.
+    if (cost < least || (cost == least && best_pair && !pair)) least = cost, best = bn, best_pair = pair;
   };
   // MN-major operands are staged 64 columns at a time; MMAs take widths of
   // multiples of 16 (a pair's of 32).
