@@ -407,7 +407,7 @@ __device__ __forceinline__ void gated_block(const Params& p, int row0, int col, 
 // the leader's `tempty`. tmB2 is Wu's map for a gated product and unused
 // otherwise.
 // ---------------------------------------------------------------------------
-template <bool PAIR, int EPI>
+template <bool PAIR, int EPI, bool WIDE>
 __global__ void __launch_bounds__(THREADS, 1)
     k_linear(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
              const __grid_constant__ CUtensorMap tmB2, const __grid_constant__ Params p) {
@@ -415,10 +415,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   constexpr bool B_MN = EPI == E_BWD || EPI == E_GATED_BWD;  // B is stored [K, N]
   constexpr int TILE_M = PAIR ? 2 * BM : BM;
   using F = Ahead<EPI>;
-  const int bn = p.t.bn, stages = p.t.stages;
+  const int bn = WIDE ? 256 : p.t.bn, stages = p.t.stages;
   const int on = GATED ? bn / 2 : bn;  // output columns of a tile
-  const uint32_t a_bytes = p.t.a_rows * (BK * 2), kb_bytes = a_bytes + p.t.b_rows * (BK * 2);
-  const int sub = p.t.sub;
+  const int b_rows = WIDE ? (PAIR ? 128 : 256) : p.t.b_rows;
+  const uint32_t a_bytes = (WIDE ? BM : p.t.a_rows) * (BK * 2), kb_bytes = a_bytes + b_rows * (BK * 2);
+  const int sub = WIDE ? 1 : p.t.sub;
   const uint32_t stage_bytes = sub * kb_bytes;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -510,7 +511,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tma_load_2d_pair(sb, mB, fb, k0, n0);
               } else {
                 tma_load_2d_pair(sb, mB, fb, n0, k0);
-                if (p.t.b_rows > 64) tma_load_2d_pair(sb + 8192, mB, fb, n0 + 64, k0);
+                if (b_rows > 64) tma_load_2d_pair(sb + 8192, mB, fb, n0 + 64, k0);
               }
             } else {
               tma_load_2d(sa, &tmA, &full[stage], k0, m0);
@@ -522,7 +523,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               } else {
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                  if (c * 64 < p.t.b_rows) tma_load_2d(sb + c * 8192, &tmB, &full[stage], n0 + c * 64, k0);
+                  if (c * 64 < b_rows) tma_load_2d(sb + c * 8192, &tmB, &full[stage], n0 + c * 64, k0);
               }
             }
           };
@@ -792,11 +793,11 @@ struct Op {
   Params p;
 };
 
-template <bool PAIR, int EPI>
+template <bool PAIR, int EPI, bool WIDE>
 int launch(Op o, int bn, int device, int num_sms, cudaStream_t st) {
   constexpr bool GATED = EPI == E_GATED, B_MN = EPI == E_BWD || EPI == E_GATED_BWD;
   constexpr int TILE_M = PAIR ? 2 * BM : BM;
-  auto kernel = k_linear<PAIR, EPI>;
+  auto kernel = k_linear<PAIR, EPI, WIDE>;
   Params& p = o.p;
   // Rows of A behind the last are not staged: an MMA then reads what lies
   // behind them in shared memory, and only its rows that are not stored see it.
@@ -899,7 +900,9 @@ int dispatch(const Op& o, cudaStream_t st) {
     for (int bn = 256; bn >= (B_MN ? 128 : 64); bn -= B_MN ? 128 : 32) consider(bn, true);
   if (family != 2)
     for (int bn = 256; bn >= (B_MN ? 64 : 32); bn -= B_MN ? 64 : 16) consider(bn, false);
-  return best_pair ? launch<true, EPI>(o, best, device, sms, st) : launch<false, EPI>(o, best, device, sms, st);
+  if (best_pair && best == 256) return launch<true, EPI, true>(o, best, device, sms, st);
+  return best_pair ? launch<true, EPI, false>(o, best, device, sms, st)
+                   : launch<false, EPI, false>(o, best, device, sms, st);
 }
 
 }  // namespace
