@@ -37,9 +37,34 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, float* red) {
   return s;
 }
 
+// A lane reads W neighbouring columns at a time, 16 bytes of the wider of the
+// two types: with eight columns of an fp32 row to a lane, each access would
+// take only half of every sector that it touches.
+template <typename X, typename Y>
+constexpr int piece() {
+  return sizeof(X) == 4 || sizeof(Y) == 4 ? 4 : 8;
+}
+
+// n columns from p on. EXACT: rows are whole pieces, so a piece is there or not
+// and its load is one predicated instruction; with the element-wise tail beside
+// it, each load would be a branch that the next one waits behind.
+template <int W, bool EXACT, typename T>
+__device__ __forceinline__ void load_piece(const T* p, int n, float (&v)[W]) {
+  if (EXACT) {
+    if (n > 0) {
+      load_n<W>(p, W, v);
+    } else {
+#pragma unroll
+      for (int e = 0; e < W; ++e) v[e] = 0.f;
+    }
+  } else {
+    load_n<W>(p, n, v);
+  }
+}
+
 // Forward: TX threads to a row (a warp up to 2048 columns, 256 threads above),
-// G pieces of eight columns to a thread.
-template <typename X, typename Y, int TX, int G>
+// G pieces of W columns to a thread.
+template <typename X, typename Y, int TX, int G, bool EXACT, int W = piece<X, Y>()>
 __global__ void __launch_bounds__(256) k_layernorm_fwd(const X* __restrict__ x, int64_t ldx, const bf16* __restrict__ g,
                                                        const bf16* __restrict__ b, Y* __restrict__ y, int64_t ldy,
                                                        float* __restrict__ mean, float* __restrict__ rstd, int T, int d,
@@ -47,47 +72,46 @@ __global__ void __launch_bounds__(256) k_layernorm_fwd(const X* __restrict__ x, 
   __shared__ float red[2][16];
   const int64_t row = (int64_t)blockIdx.x * (256 / TX) + threadIdx.x / TX;
   const int tx = threadIdx.x % TX;
-  const bool ok = row < T;
-  if (TX == 32 && !ok) return;  // no barrier below; wider rows have one row to a block
+  if (TX == 32 && row >= T) return;  // no barrier below; wider rows have one row to a block
   const X* xr = x + row * ldx;
-  float v[G][8];
+  float v[G][W];
   float s = 0.f;
 #pragma unroll
   for (int k = 0; k < G; ++k) {
-    const int c = (tx + k * TX) * 8;
-    load8n(xr + c, d - c, v[k]);
+    const int c = (tx + k * TX) * W;
+    load_piece<W, EXACT>(xr + c, d - c, v[k]);
   }
 #pragma unroll
   for (int k = 0; k < G; ++k)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s += v[k][e];
+    for (int e = 0; e < W; ++e) s += v[k][e];
   const float m = row_sum2<TX>(s, 0.f, red[0]).x / (float)d;
   float q = 0.f;
 #pragma unroll
   for (int k = 0; k < G; ++k) {
-    const int n = d - (tx + k * TX) * 8;
+    const int n = d - (tx + k * TX) * W;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float t = e < n ? v[k][e] - m : 0.f;
+    for (int e = 0; e < W; ++e) {
+      const float t = (EXACT ? n > 0 : e < n) ? v[k][e] - m : 0.f;
       q += t * t;
     }
   }
   const float r = rsqrtf(row_sum2<TX>(q, 0.f, red[1]).x / (float)d + eps);
 #pragma unroll
   for (int k = 0; k < G; ++k) {
-    const int c = (tx + k * TX) * 8;
+    const int c = (tx + k * TX) * W;
     if (c >= d) continue;
-    float gv[8], bv[8];
-    load8n(g + c, d - c, gv);
+    float gv[W], bv[W];
+    load_n<W>(g + c, EXACT ? W : d - c, gv);
     if (b) {
-      load8n(b + c, d - c, bv);
+      load_n<W>(b + c, EXACT ? W : d - c, bv);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) bv[e] = 0.f;
+      for (int e = 0; e < W; ++e) bv[e] = 0.f;
     }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[k][e] = (v[k][e] - m) * r * gv[e] + bv[e];
-    store8n(y + row * ldy + c, d - c, v[k]);
+    for (int e = 0; e < W; ++e) v[k][e] = (v[k][e] - m) * r * gv[e] + bv[e];
+    store_n<W>(y + row * ldy + c, EXACT ? W : d - c, v[k]);
   }
   if (tx == 0) {
     if (mean) mean[row] = m;
@@ -98,7 +122,7 @@ __global__ void __launch_bounds__(256) k_layernorm_fwd(const X* __restrict__ x, 
 // Backward: a block of 256 threads takes a run of rows, RY = 256 / TX at a
 // time; a thread keeps its columns' sums of dg and db over all of them. The
 // block's sums go to its own row [dg | db] of `part`.
-template <typename X, typename Y, int TX, int G>
+template <typename X, typename Y, int TX, int G, bool EXACT, int W = piece<X, Y>()>
 __global__ void __launch_bounds__(256) k_layernorm_bwd(const X* __restrict__ x, int64_t ldx, const bf16* __restrict__ g,
                                                        const float* __restrict__ mean, const float* __restrict__ rstd,
                                                        const Y* __restrict__ dy, int64_t lddy, const X* dres,
@@ -106,18 +130,15 @@ __global__ void __launch_bounds__(256) k_layernorm_bwd(const X* __restrict__ x, 
                                                        float* __restrict__ part, int T, int d, int rows_per_block) {
   constexpr int RY = 256 / TX;
   __shared__ float red[2][16];
-  __shared__ float col[RY > 1 ? RY - 1 : 1][RY > 1 ? TX * G * 8 : 1];
+  __shared__ float col[RY > 1 ? RY - 1 : 1][RY > 1 ? TX * G * W : 1];
   const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
-  float ag[G][8], ab[G][8];
-  uint4 gp[G];
+  float ag[G][W], ab[G][W], gv[G][W];
 #pragma unroll
   for (int k = 0; k < G; ++k) {
-    const int c = (tx + k * TX) * 8;
-    float gv[8];
-    load8n(g + c, d - c, gv);
-    gp[k] = pack8(gv);
+    const int c = (tx + k * TX) * W;
+    load_piece<W, EXACT>(g + c, d - c, gv[k]);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ag[k][e] = ab[k][e] = 0.f;
+    for (int e = 0; e < W; ++e) ag[k][e] = ab[k][e] = 0.f;
   }
   const int64_t r0 = (int64_t)blockIdx.x * rows_per_block;
   const int64_t r1 = min((int64_t)T, r0 + rows_per_block);
@@ -125,25 +146,23 @@ __global__ void __launch_bounds__(256) k_layernorm_bwd(const X* __restrict__ x, 
   for (int64_t base = r0; base < r1; base += RY, half ^= 1) {
     const int64_t row = base + ty;
     const bool ok = row < r1;
-    float xv[G][8], dv[G][8], rv[G][8];
+    float xv[G][W], dv[G][W], rv[G][W];
     const float m = ok ? mean[row] : 0.f, r = ok ? rstd[row] : 0.f;
 #pragma unroll
     for (int k = 0; k < G; ++k) {
-      const int c = (tx + k * TX) * 8, n = ok ? d - c : 0;
-      load8n(x + row * ldx + c, n, xv[k]);
-      load8n(dy + row * lddy + c, n, dv[k]);
-      if (dres) load8n(dres + row * lddres + c, n, rv[k]);
+      const int c = (tx + k * TX) * W, n = ok ? d - c : 0;
+      load_piece<W, EXACT>(x + row * ldx + c, n, xv[k]);
+      load_piece<W, EXACT>(dy + row * lddy + c, n, dv[k]);
+      if (dres) load_piece<W, EXACT>(dres + row * lddres + c, n, rv[k]);
     }
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int k = 0; k < G; ++k) {
-      const int n = d - (tx + k * TX) * 8;
-      float gv[8];
-      unpack8(gp[k], gv);
+      const int n = d - (tx + k * TX) * W;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float xh = ok && e < n ? (xv[k][e] - m) * r : 0.f;
-        const float w = dv[k][e] * gv[e];
+      for (int e = 0; e < W; ++e) {
+        const float xh = ok && (EXACT ? n > 0 : e < n) ? (xv[k][e] - m) * r : 0.f;
+        const float w = dv[k][e] * gv[k][e];
         xv[k][e] = xh;
         s1 += w;
         s2 += w * xh;
@@ -156,17 +175,16 @@ __global__ void __launch_bounds__(256) k_layernorm_bwd(const X* __restrict__ x, 
     if (ok) {
 #pragma unroll
       for (int k = 0; k < G; ++k) {
-        const int c = (tx + k * TX) * 8;
+        const int c = (tx + k * TX) * W;
         if (c >= d) continue;
-        float gv[8], o[8];
-        unpack8(gp[k], gv);
+        float o[W];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          o[e] = r * (dv[k][e] * gv[e] - m1 - xv[k][e] * m2);
+        for (int e = 0; e < W; ++e) {
+          o[e] = r * (dv[k][e] * gv[k][e] - m1 - xv[k][e] * m2);
           if (dres) o[e] += rv[k][e];
         }
-        store8n(dx + row * lddx + c, d - c, o);
-        if (dx_bf16) store8n(dx_bf16 + row * lddx + c, d - c, o);
+        store_n<W>(dx + row * lddx + c, EXACT ? W : d - c, o);
+        if (dx_bf16) store_n<W>(dx_bf16 + row * lddx + c, EXACT ? W : d - c, o);
       }
     }
   }
@@ -174,26 +192,26 @@ __global__ void __launch_bounds__(256) k_layernorm_bwd(const X* __restrict__ x, 
   float* out = part + (int64_t)blockIdx.x * 2 * d;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
-    float(&acc)[G][8] = which ? ab : ag;
+    float(&acc)[G][W] = which ? ab : ag;
     if (RY > 1) {
       __syncthreads();
       if (ty > 0) {
 #pragma unroll
         for (int k = 0; k < G; ++k)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) col[ty - 1][(k * 8 + e) * TX + tx] = acc[k][e];
+          for (int e = 0; e < W; ++e) col[ty - 1][(k * W + e) * TX + tx] = acc[k][e];
       }
       __syncthreads();
     }
     if (ty == 0) {
 #pragma unroll
       for (int k = 0; k < G; ++k) {
-        const int c = (tx + k * TX) * 8;
+        const int c = (tx + k * TX) * W;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < W; ++e) {
           float s = acc[k][e];
 #pragma unroll
-          for (int i = 0; i < RY - 1; ++i) s += col[i][(k * 8 + e) * TX + tx];
+          for (int i = 0; i < RY - 1; ++i) s += col[i][(k * W + e) * TX + tx];
           if (c + e < d) out[which * d + c + e] = s;
         }
       }
@@ -225,7 +243,8 @@ __global__ void __launch_bounds__(1024) k_column_sums(const float* __restrict__ 
   }
 }
 
-constexpr int kLnMaxBlocks = 592;
+// Blocks of the backward: two to each of 148 SMs, which its registers allow.
+constexpr int kLnMaxBlocks = 296;
 
 int ln_bwd_blocks(int T) { return T < kLnMaxBlocks ? (T > 0 ? T : 1) : kLnMaxBlocks; }
 
@@ -233,15 +252,17 @@ template <typename X, typename Y, int TX, int G>
 int ln_fwd_launch(const void* x, int64_t ldx, const void* g, const void* b, void* y, int64_t ldy, float* mean,
                   float* rstd, int T, int d, float eps, cudaStream_t st) {
   const int rpb = 256 / TX;
-  k_layernorm_fwd<X, Y, TX, G><<<(T + rpb - 1) / rpb, 256, 0, st>>>((const X*)x, ldx, (const bf16*)g, (const bf16*)b,
-                                                                  (Y*)y, ldy, mean, rstd, T, d, eps);
+  auto k = d % piece<X, Y>() ? k_layernorm_fwd<X, Y, TX, G, false> : k_layernorm_fwd<X, Y, TX, G, true>;
+  k<<<(T + rpb - 1) / rpb, 256, 0, st>>>((const X*)x, ldx, (const bf16*)g, (const bf16*)b, (Y*)y, ldy, mean, rstd, T, d,
+                                         eps);
   return launch_status();
 }
 
 template <typename X, typename Y>
 int ln_fwd(const void* x, int64_t ldx, const void* g, const void* b, void* y, int64_t ldy, float* mean, float* rstd,
            int T, int d, float eps, cudaStream_t st) {
-#define MT_LN_FWD(TX, G) return ln_fwd_launch<X, Y, TX, G>(x, ldx, g, b, y, ldy, mean, rstd, T, d, eps, st)
+  constexpr int P = 8 / piece<X, Y>();  // pieces of a lane for each eight columns
+#define MT_LN_FWD(TX, G) return ln_fwd_launch<X, Y, TX, G * P>(x, ldx, g, b, y, ldy, mean, rstd, T, d, eps, st)
   if (d <= 256) MT_LN_FWD(32, 1);
   if (d <= 512) MT_LN_FWD(32, 2);
   if (d <= 1024) MT_LN_FWD(32, 4);
@@ -256,22 +277,23 @@ template <typename X, typename Y, int TX, int G>
 int ln_bwd_launch(const LayerNormBwd& a, cudaStream_t st) {
   const int nb = ln_bwd_blocks(a.T);
   const int rpb = (a.T + nb - 1) / nb;
-  k_layernorm_bwd<X, Y, TX, G><<<nb, 256, 0, st>>>((const X*)a.x, a.ldx, (const bf16*)a.g, a.mean, a.rstd,
-                                                   (const Y*)a.dy, a.lddy, (const X*)a.dres, a.lddres, (X*)a.dx,
-                                                   (bf16*)a.dx_bf16, a.lddx, a.part, a.T, a.d, rpb);
+  auto k = a.d % piece<X, Y>() ? k_layernorm_bwd<X, Y, TX, G, false> : k_layernorm_bwd<X, Y, TX, G, true>;
+  k<<<nb, 256, 0, st>>>((const X*)a.x, a.ldx, (const bf16*)a.g, a.mean, a.rstd, (const Y*)a.dy, a.lddy, (const X*)a.dres,
+                        a.lddres, (X*)a.dx, (bf16*)a.dx_bf16, a.lddx, a.part, a.T, a.d, rpb);
   if (const int rc = launch_status()) return rc;
   return launch_column_sums(a.part, nb, 2 * (int64_t)a.d, 2 * a.d, a.dg, a.d, a.db, st);
 }
 
 template <typename X, typename Y>
 int ln_bwd(const LayerNormBwd& a, cudaStream_t st) {
-  if (a.d <= 256) return ln_bwd_launch<X, Y, 32, 1>(a, st);
-  if (a.d <= 512) return ln_bwd_launch<X, Y, 64, 1>(a, st);
-  if (a.d <= 1024) return ln_bwd_launch<X, Y, 128, 1>(a, st);
-  if (a.d <= 2048) return ln_bwd_launch<X, Y, 256, 1>(a, st);
-  if (a.d <= 4096) return ln_bwd_launch<X, Y, 256, 2>(a, st);
-  if (a.d <= 6144) return ln_bwd_launch<X, Y, 256, 3>(a, st);
-  return ln_bwd_launch<X, Y, 256, 4>(a, st);
+  constexpr int P = 8 / piece<X, Y>();
+  if (a.d <= 256) return ln_bwd_launch<X, Y, 32, P>(a, st);
+  if (a.d <= 512) return ln_bwd_launch<X, Y, 64, P>(a, st);
+  if (a.d <= 1024) return ln_bwd_launch<X, Y, 128, P>(a, st);
+  if (a.d <= 2048) return ln_bwd_launch<X, Y, 256, P>(a, st);
+  if (a.d <= 4096) return ln_bwd_launch<X, Y, 256, 2 * P>(a, st);
+  if (a.d <= 6144) return ln_bwd_launch<X, Y, 256, 3 * P>(a, st);
+  return ln_bwd_launch<X, Y, 256, 4 * P>(a, st);
 }
 
 }  // namespace
