@@ -186,36 +186,37 @@ struct DropDesc {
   uint32_t threshold;  // an element is kept when its word is >= this
   float scale;         // 1 / (1 - p)
   uint32_t row0;
-  uint64_t seed, offset;
+  uint64_t offset;
   const int64_t* offset_dev;  // added to offset when the kernel runs; may be NULL
+  // The ten rounds' keys, which depend on the seed alone: as kernel parameters
+  // they are constant operands of the rounds, not 20 additions beside them.
+  uint32_t key0[10], key1[10];
 };
 
-// The parts of the counter and key that a kernel's threads share.
+// The offset's halves, which a kernel's threads share.
 struct DropKey {
-  uint32_t k0, k1, c2, c3;
+  uint32_t c2, c3;
 };
 __device__ __forceinline__ DropKey drop_key(const DropDesc& d) {
   const uint64_t off = d.offset + (d.on && d.offset_dev ? (uint64_t)*d.offset_dev : 0ull);
-  return DropKey{(uint32_t)d.seed, (uint32_t)(d.seed >> 32), (uint32_t)off, (uint32_t)(off >> 32)};
+  return DropKey{(uint32_t)off, (uint32_t)(off >> 32)};
 }
-__device__ __forceinline__ uint4 philox4x32(uint32_t c0, uint32_t c1, const DropKey& k) {
-  uint32_t x0 = c0, x1 = c1, x2 = k.c2, x3 = k.c3, k0 = k.k0, k1 = k.k1;
+__device__ __forceinline__ uint4 philox4x32(uint32_t c0, uint32_t c1, const DropDesc& d, const DropKey& k) {
+  uint32_t x0 = c0, x1 = c1, x2 = k.c2, x3 = k.c3;
 #pragma unroll
   for (int i = 0; i < 10; ++i) {
     const uint64_t a = (uint64_t)x0 * 0xD2511F53u, b = (uint64_t)x2 * 0xCD9E8D57u;
-    x0 = (uint32_t)(b >> 32) ^ x1 ^ k0;
+    x0 = (uint32_t)(b >> 32) ^ x1 ^ d.key0[i];
     x1 = (uint32_t)b;
-    x2 = (uint32_t)(a >> 32) ^ x3 ^ k1;
+    x2 = (uint32_t)(a >> 32) ^ x3 ^ d.key1[i];
     x3 = (uint32_t)a;
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
   }
   return make_uint4(x0, x1, x2, x3);
 }
 // v[0..3], columns 4 q .. 4 q + 3 of a row: a dropped element becomes 0
 // whatever it held (NaN and infinities too), a kept one is scaled.
 __device__ __forceinline__ void drop4(float* v, uint32_t q, uint32_t row, const DropDesc& d, const DropKey& k) {
-  const uint4 w = philox4x32(q, row, k);
+  const uint4 w = philox4x32(q, row, d, k);
   v[0] = w.x >= d.threshold ? v[0] * d.scale : 0.f;
   v[1] = w.y >= d.threshold ? v[1] * d.scale : 0.f;
   v[2] = w.z >= d.threshold ? v[2] * d.scale : 0.f;
@@ -225,7 +226,7 @@ __device__ __forceinline__ void drop4(float* v, uint32_t q, uint32_t row, const 
 // Host: the kernels' description of a caller's dropout for `rows` rows, or
 // MT_ERR_ARG: p outside [0, 1) or NaN, rows outside the counter's 32 bits.
 inline int make_drop(const mt_dropout* u, int64_t rows, DropDesc* out) {
-  *out = DropDesc{0, 0, 1.f, 0, 0, 0, nullptr};
+  *out = DropDesc{0, 0, 1.f, 0, 0, nullptr, {}, {}};
   if (!u) return MT_OK;
   if (!(u->p >= 0.f) || !(u->p < 1.f)) return MT_ERR_ARG;
   if (u->row0 < 0 || u->row0 + rows > (int64_t(1) << 32)) return MT_ERR_ARG;
@@ -234,9 +235,12 @@ inline int make_drop(const mt_dropout* u, int64_t rows, DropDesc* out) {
   out->threshold = (uint32_t)llrint((double)u->p * 4294967296.0);
   out->scale = (float)(1.0 / (1.0 - (double)u->p));
   out->row0 = (uint32_t)u->row0;
-  out->seed = (uint64_t)u->seed;
   out->offset = (uint64_t)u->offset;
   out->offset_dev = u->offset_dev;
+  for (uint32_t i = 0; i < 10; ++i) {
+    out->key0[i] = (uint32_t)u->seed + i * 0x9E3779B9u;
+    out->key1[i] = (uint32_t)((uint64_t)u->seed >> 32) + i * 0xBB67AE85u;
+  }
   return MT_OK;
 }
 

@@ -25,7 +25,9 @@ int pick_tx(int cols, int w) {
   return best;
 }
 
-constexpr int ROWS = 4;  // rows that a thread has in flight
+// Rows that a thread has in flight, W columns of each.
+template <int W>
+constexpr int ROWS = 8 / W;
 
 template <int W>
 __device__ __forceinline__ void drop_piece(float (&v)[W], int col, uint32_t row, const DropDesc& drop, const DropKey& key) {
@@ -39,25 +41,25 @@ template <typename X, typename Y, int W, bool WHOLE>
 __device__ __forceinline__ void dropout_rows(const X* x, int64_t ldx, const DropDesc& drop, const DropKey& key,
                                              const Y* res, int64_t ldr, Y* y, int64_t ldy, int64_t base, int ry, int T,
                                              int c, int n) {
-  float v[ROWS][W], r[ROWS][W];
+  float v[ROWS<W>][W], r[ROWS<W>][W];
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
+  for (int i = 0; i < ROWS<W>; ++i) {
     const int64_t t = base + i * ry;
     if (WHOLE || t < T) load_n<W>(x + t * ldx + c, WHOLE ? W : n, v[i]);
   }
   if (res) {
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
+    for (int i = 0; i < ROWS<W>; ++i) {
       const int64_t t = base + i * ry;
       if (WHOLE || t < T) load_n<W>(res + t * ldr + c, WHOLE ? W : n, r[i]);
     }
   }
   if (drop.on) {
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) drop_piece<W>(v[i], c, drop.row0 + (uint32_t)(base + i * ry), drop, key);
+    for (int i = 0; i < ROWS<W>; ++i) drop_piece<W>(v[i], c, drop.row0 + (uint32_t)(base + i * ry), drop, key);
   }
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
+  for (int i = 0; i < ROWS<W>; ++i) {
     const int64_t t = base + i * ry;
     if (res) {
 #pragma unroll
@@ -68,16 +70,16 @@ __device__ __forceinline__ void dropout_rows(const X* x, int64_t ldx, const Drop
 }
 
 template <typename X, typename Y, int W>
-__global__ void __launch_bounds__(256) k_dropout(const X* x, int64_t ldx, const DropDesc drop, const Y* res, int64_t ldr,
+__global__ void __launch_bounds__(256, 4) k_dropout(const X* x, int64_t ldx, const DropDesc drop, const Y* res, int64_t ldr,
                                                  Y* y, int64_t ldy, int T, int d, int tx_log2) {
   const int tx = threadIdx.x & ((1 << tx_log2) - 1), ry = 256 >> tx_log2;
   const int c = (((int)blockIdx.x << tx_log2) + tx) * W;
   if (c >= d) return;
   const int n = d - c;
   const DropKey key = drop_key(drop);
-  const int64_t step = (int64_t)gridDim.y * ry * ROWS;
-  for (int64_t base = (int64_t)blockIdx.y * ry * ROWS + (threadIdx.x >> tx_log2); base < T; base += step) {
-    if (n >= W && base + (ROWS - 1) * ry < T)
+  const int64_t step = (int64_t)gridDim.y * ry * ROWS<W>;
+  for (int64_t base = (int64_t)blockIdx.y * ry * ROWS<W> + (threadIdx.x >> tx_log2); base < T; base += step) {
+    if (n >= W && base + (ROWS<W> - 1) * ry < T)
       dropout_rows<X, Y, W, true>(x, ldx, drop, key, res, ldr, y, ldy, base, ry, T, c, n);
     else
       dropout_rows<X, Y, W, false>(x, ldx, drop, key, res, ldr, y, ldy, base, ry, T, c, n);
@@ -88,9 +90,9 @@ template <typename X, int ACT, int W, bool WHOLE>
 __device__ __forceinline__ void act_bwd_rows(const X* dc, int64_t lddc, const bf16* z, int64_t ldz, const DropDesc& drop,
                                              const DropKey& key, bf16* dz, int64_t lddz, int64_t base, int ry,
                                              int64_t end, int c, int n, float (&acc)[W]) {
-  float v[ROWS][W], zv[ROWS][W];
+  float v[ROWS<W>][W], zv[ROWS<W>][W];
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
+  for (int i = 0; i < ROWS<W>; ++i) {
     const int64_t t = base + i * ry;
     if (WHOLE || t < end) {
       load_n<W>(dc + t * lddc + c, WHOLE ? W : n, v[i]);
@@ -98,7 +100,7 @@ __device__ __forceinline__ void act_bwd_rows(const X* dc, int64_t lddc, const bf
     }
   }
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
+  for (int i = 0; i < ROWS<W>; ++i) {
     const int64_t t = base + i * ry;
     if (!WHOLE && t >= end) break;
     if (ACT != MT_ACT_NONE) {
@@ -114,7 +116,7 @@ __device__ __forceinline__ void act_bwd_rows(const X* dc, int64_t lddc, const bf
 }
 
 template <typename X, int ACT, int W>
-__global__ void __launch_bounds__(256) k_act_bwd(const X* dc, int64_t lddc, const bf16* z, int64_t ldz,
+__global__ void __launch_bounds__(256, 4) k_act_bwd(const X* dc, int64_t lddc, const bf16* z, int64_t ldz,
                                                  const DropDesc drop, bf16* dz, int64_t lddz, float* __restrict__ part,
                                                  int M, int N, int rows_per_block, int tx_log2) {
   __shared__ float sh[256 * W];
@@ -127,8 +129,8 @@ __global__ void __launch_bounds__(256) k_act_bwd(const X* dc, int64_t lddc, cons
   for (int e = 0; e < W; ++e) acc[e] = 0.f;
   const int64_t r0 = (int64_t)blockIdx.y * rows_per_block, r1 = min((int64_t)M, r0 + rows_per_block);
   if (n > 0) {
-    for (int64_t base = r0 + ty; base < r1; base += ry * ROWS) {
-      if (n >= W && base + (ROWS - 1) * ry < r1)
+    for (int64_t base = r0 + ty; base < r1; base += ry * ROWS<W>) {
+      if (n >= W && base + (ROWS<W> - 1) * ry < r1)
         act_bwd_rows<X, ACT, W, true>(dc, lddc, z, ldz, drop, key, dz, lddz, base, ry, r1, c, n, acc);
       else
         act_bwd_rows<X, ACT, W, false>(dc, lddc, z, ldz, drop, key, dz, lddz, base, ry, r1, c, n, acc);
@@ -158,26 +160,33 @@ struct Grid {
   int tx_log2, gx, gy, rows_per_block;
 };
 
-// About 8 blocks for each of 148 SMs, and at least ROWS rows to a thread.
-Grid grid_for(int rows, int cols, int w) {
+// At most `blocks` blocks, and at least ROWS rows to a thread.
+Grid grid_for(int rows, int cols, int w, int blocks) {
   Grid g;
-  const int tx = pick_tx(cols, w), ry = 256 / tx;
+  const int tx = pick_tx(cols, w), ry = 256 / tx, deep = 8 / w;
   g.tx_log2 = log2_of(tx);
   g.gx = ((cols + w - 1) / w + tx - 1) / tx;
-  const int most = (rows + ry * ROWS - 1) / (ry * ROWS);
-  const int want = (148 * 8 + g.gx - 1) / g.gx;
+  const int most = (rows + ry * deep - 1) / (ry * deep);
+  const int want = blocks / g.gx > 1 ? blocks / g.gx : 1;
   g.gy = most < want ? most : want;
-  if (g.gy > 1024) g.gy = 1024;
+  if (g.gy > 65535) g.gy = 65535;
   if (g.gy < 1) g.gy = 1;
   g.rows_per_block = (rows + g.gy - 1) / g.gy;
   return g;
 }
 
+// Dropout: many short blocks, which leave no ragged last wave (8 to an SM took
+// 84 us on 8192 x 5120 with a residual, 32 take 74).
+constexpr int kDropoutBlocks = 148 * 32;
+// The backward's blocks each leave a row of partial column sums, so there are
+// only as many as run at once.
+constexpr int kActBwdBlocks = 148 * 4;
+
 template <typename X, typename Y>
 int dropout_launch(const void* x, int64_t ldx, const DropDesc& drop, const void* res, int64_t ldr, void* y, int64_t ldy,
                    int T, int d, cudaStream_t st) {
   constexpr int W = sizeof(X) == 4 || sizeof(Y) == 4 ? 4 : 8;
-  const Grid g = grid_for(T, d, W);
+  const Grid g = grid_for(T, d, W, kDropoutBlocks);
   k_dropout<X, Y, W><<<dim3(g.gx, g.gy), 256, 0, st>>>((const X*)x, ldx, drop, (const Y*)res, ldr, (Y*)y, ldy, T, d,
                                                     g.tx_log2);
   return launch_status();
@@ -187,7 +196,7 @@ template <typename X>
 int act_bwd_launch(const void* dc, int64_t lddc, const void* z, int64_t ldz, int act, const DropDesc& drop, void* dz,
                    int64_t lddz, float* part, float* db, int M, int N, cudaStream_t st) {
   constexpr int W = sizeof(X) == 4 ? 4 : 8;
-  const Grid g = grid_for(M, N, W);
+  const Grid g = grid_for(M, N, W, kActBwdBlocks);
   float* p = db ? part : nullptr;
   MT_WITH_ACT(act, (k_act_bwd<X, ACT, W><<<dim3(g.gx, g.gy), 256, 0, st>>>((const X*)dc, lddc, (const bf16*)z, ldz, drop,
                                                                        (bf16*)dz, lddz, p, M, N, g.rows_per_block,
@@ -209,7 +218,7 @@ int launch_dropout(const void* x, int x_type, int64_t ldx, const DropDesc& drop,
 }
 
 size_t act_bwd_partial_floats(int M, int N) {
-  const int a = grid_for(M, N, 4).gy, b = grid_for(M, N, 8).gy;  // dc's type is not known here
+  const int a = grid_for(M, N, 4, kActBwdBlocks).gy, b = grid_for(M, N, 8, kActBwdBlocks).gy;  // dc's type is not known here
   return (size_t)(a > b ? a : b) * N;
 }
 

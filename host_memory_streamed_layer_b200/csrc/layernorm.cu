@@ -70,9 +70,10 @@ __global__ void __launch_bounds__(256) k_layernorm_fwd(const X* __restrict__ x, 
                                                        float* __restrict__ mean, float* __restrict__ rstd, int T, int d,
                                                        float eps) {
   __shared__ float red[2][16];
-  const int64_t row = (int64_t)blockIdx.x * (256 / TX) + threadIdx.x / TX;
+  const int64_t row_ = (int64_t)blockIdx.x * (256 / TX) + threadIdx.x / TX;
   const int tx = threadIdx.x % TX;
-  if (TX == 32 && row >= T) return;  // no barrier below; wider rows have one row to a block
+  if (TX == 32 && row_ >= T) return;  // no barrier below
+  const int64_t row = TX == 32 || row_ < T ? row_ : T - 1;  // a wider row's threads all stay for the barriers
   const X* xr = x + row * ldx;
   float v[G][W];
   float s = 0.f;
@@ -266,7 +267,7 @@ int ln_fwd(const void* x, int64_t ldx, const void* g, const void* b, void* y, in
   if (d <= 256) MT_LN_FWD(32, 1);
   if (d <= 512) MT_LN_FWD(32, 2);
   if (d <= 1024) MT_LN_FWD(32, 4);
-  if (d <= 2048) MT_LN_FWD(32, 8);
+  if (d <= 2048) MT_LN_FWD(128, 2);
   if (d <= 4096) MT_LN_FWD(256, 2);
   if (d <= 6144) MT_LN_FWD(256, 3);
   MT_LN_FWD(256, 4);
