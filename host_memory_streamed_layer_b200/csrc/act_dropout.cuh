@@ -13,6 +13,8 @@ namespace mt {
 
 typedef __nv_bfloat16 bf16;
 
+constexpr int kMaxDevices = 64;  // of what a launcher keeps per device
+
 // ---------------------------------------------------------------------------
 // Eight consecutive elements of a row, as fp32. The row pieces start on
 // 16-byte boundaries (row bases and pitches do); a piece cut short by the

@@ -120,18 +120,43 @@ __global__ void __launch_bounds__(256) k_layernorm_fwd(const X* __restrict__ x, 
   }
 }
 
-// Backward: a block of 256 threads takes a run of rows, RY = 256 / TX at a
-// time; a thread keeps its columns' sums of dg and db over all of them. The
-// block's sums go to its own row [dg | db] of `part`.
-template <typename X, typename Y, int TX, int G, bool EXACT, int W = piece<X, Y>()>
-__global__ void __launch_bounds__(256) k_layernorm_bwd(const X* __restrict__ x, int64_t ldx, const bf16* __restrict__ g,
-                                                       const float* __restrict__ mean, const float* __restrict__ rstd,
-                                                       const Y* __restrict__ dy, int64_t lddy, const X* dres,
-                                                       int64_t lddres, X* dx, bf16* dx_bf16, int64_t lddx,
-                                                       float* __restrict__ part, int T, int d, int rows_per_block) {
-  constexpr int RY = 256 / TX;
-  __shared__ float red[2][16];
-  __shared__ float col[RY > 1 ? RY - 1 : 1][RY > 1 ? TX * G * W : 1];
+// Backward: a block takes a run of rows, RY at a time with TX threads to each;
+// a thread keeps its columns' sums of dg and db over all of them. The block's
+// sums go to its own row [dg | db] of `part`.
+//
+// Rows are copied into shared memory STAGES row groups ahead. A lane copies the
+// very pieces that it reads back, so a copy needs no barrier, and the registers
+// hold the sums instead of loads in flight: with the loads in registers,
+// 8192 x 5120 took 155 us (one block to an SM), 16384 x 2048 took 110 us.
+template <typename X, typename Y, int TX, int G>
+struct LnBwd {
+  static constexpr int W = piece<X, Y>();
+  static constexpr int THREADS = TX > 256 ? TX : 256;
+  static constexpr int RY = THREADS / TX;
+  static constexpr int PX = W * sizeof(X), PY = W * sizeof(Y);  // bytes of a piece
+  static constexpr int ROWS_BYTES = THREADS * G * (2 * PX + PY);  // x, dres and dy of a row group
+  static constexpr int STAGES = ROWS_BYTES <= 28672 ? 4 : ROWS_BYTES <= 75776 ? 3 : 2;
+  static constexpr int SMEM = STAGES * ROWS_BYTES;
+  static constexpr int PER_SM = SMEM <= 112 * 1024 ? 2 : 1;
+};
+
+template <typename T, int W>
+__device__ __forceinline__ void copy_piece(uint32_t dst, const T* src) {
+  if (W * sizeof(T) == 16)
+    copy16(dst, src);
+  else
+    copy8(dst, src);
+}
+
+template <typename X, typename Y, int TX, int G, bool EXACT>
+__global__ void __launch_bounds__(LnBwd<X, Y, TX, G>::THREADS, LnBwd<X, Y, TX, G>::PER_SM)
+    k_layernorm_bwd(const X* x, int64_t ldx, const bf16* __restrict__ g, const float* __restrict__ mean,
+                    const float* __restrict__ rstd, const Y* dy, int64_t lddy, const X* dres, int64_t lddres, X* dx,
+                    bf16* dx_bf16, int64_t lddx, float* __restrict__ part, int T, int d, int rows_per_block) {
+  using L = LnBwd<X, Y, TX, G>;
+  constexpr int W = L::W, RY = L::RY, S = L::STAGES;
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float red[2][L::THREADS / 16];
   const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
   float ag[G][W], ab[G][W], gv[G][W];
 #pragma unroll
@@ -143,18 +168,54 @@ __global__ void __launch_bounds__(256) k_layernorm_bwd(const X* __restrict__ x, 
   }
   const int64_t r0 = (int64_t)blockIdx.x * rows_per_block;
   const int64_t r1 = min((int64_t)T, r0 + rows_per_block);
-  int half = 0;
-  for (int64_t base = r0; base < r1; base += RY, half ^= 1) {
-    const int64_t row = base + ty;
+  const int groups = r1 > r0 ? (int)((r1 - r0 + RY - 1) / RY) : 0;
+  // This lane's slots of a stage: G pieces of x, of dres, of dy.
+  const uint32_t mine = smem_u32(ring) + threadIdx.x * L::PX, mine_y = smem_u32(ring) + L::THREADS * G * 2 * L::PX + threadIdx.x * L::PY;
+  auto fetch = [&](int i) {  // row group i, one group of copies (empty behind the last)
+    const int64_t row = r0 + (int64_t)i * RY + ty;
+    if (EXACT && i < groups && row < r1) {
+      const uint32_t at = i % S * L::ROWS_BYTES;
+#pragma unroll
+      for (int k = 0; k < G; ++k) {
+        const int c = (tx + k * TX) * W;
+        if (c >= d) break;
+        copy_piece<X, W>(mine + at + k * L::THREADS * L::PX, x + row * ldx + c);
+        copy_piece<Y, W>(mine_y + at + k * L::THREADS * L::PY, dy + row * lddy + c);
+        if (dres) copy_piece<X, W>(mine + at + (G + k) * L::THREADS * L::PX, dres + row * lddres + c);
+      }
+    }
+    copy_commit();
+  };
+  if (EXACT) {
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) fetch(i);
+  }
+  float next_m = 0.f, next_r = 0.f;
+  if (r0 + ty < r1) next_m = mean[r0 + ty], next_r = rstd[r0 + ty];
+  for (int i = 0; i < groups; ++i) {
+    const int64_t row = r0 + (int64_t)i * RY + ty;
     const bool ok = row < r1;
+    const float m = next_m, r = next_r;
+    if (row + RY < r1) next_m = mean[row + RY], next_r = rstd[row + RY];
     float xv[G][W], dv[G][W], rv[G][W];
-    const float m = ok ? mean[row] : 0.f, r = ok ? rstd[row] : 0.f;
+    if (EXACT) {
+      fetch(i + S - 1);
+      copy_wait<S - 1>();
+    }
 #pragma unroll
     for (int k = 0; k < G; ++k) {
       const int c = (tx + k * TX) * W, n = ok ? d - c : 0;
-      load_piece<W, EXACT>(x + row * ldx + c, n, xv[k]);
-      load_piece<W, EXACT>(dy + row * lddy + c, n, dv[k]);
-      if (dres) load_piece<W, EXACT>(dres + row * lddres + c, n, rv[k]);
+      if (EXACT) {
+        const uint8_t* at = ring + i % S * L::ROWS_BYTES + threadIdx.x * L::PX + k * L::THREADS * L::PX;
+        const uint8_t* at_y = ring + i % S * L::ROWS_BYTES + L::THREADS * (G * 2 * L::PX + k * L::PY) + threadIdx.x * L::PY;
+        load_piece<W, true>(reinterpret_cast<const X*>(at), n, xv[k]);
+        load_piece<W, true>(reinterpret_cast<const Y*>(at_y), n, dv[k]);
+        if (dres) load_piece<W, true>(reinterpret_cast<const X*>(at + G * L::THREADS * L::PX), n, rv[k]);
+      } else {
+        load_n<W>(x + row * ldx + c, n, xv[k]);
+        load_n<W>(dy + row * lddy + c, n, dv[k]);
+        if (dres) load_n<W>(dres + row * lddres + c, n, rv[k]);
+      }
     }
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
@@ -171,7 +232,7 @@ __global__ void __launch_bounds__(256) k_layernorm_bwd(const X* __restrict__ x, 
         ab[k][e] += dv[k][e];
       }
     }
-    const float2 s = row_sum2<TX>(s1, s2, red[half]);  // the halves alternate: one barrier a row
+    const float2 s = row_sum2<TX>(s1, s2, red[i & 1]);  // the halves alternate: one barrier a row group
     const float m1 = s.x / (float)d, m2 = s.y / (float)d;
     if (ok) {
 #pragma unroll
@@ -189,7 +250,9 @@ __global__ void __launch_bounds__(256) k_layernorm_bwd(const X* __restrict__ x, 
       }
     }
   }
+  copy_wait<0>();
   // The RY rows' sums meet in shared memory, in the order of ty: dg, then db.
+  float* col = reinterpret_cast<float*>(ring);  // [RY - 1][G W][TX], at most as large as a stage
   float* out = part + (int64_t)blockIdx.x * 2 * d;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
@@ -200,7 +263,7 @@ __global__ void __launch_bounds__(256) k_layernorm_bwd(const X* __restrict__ x, 
 #pragma unroll
         for (int k = 0; k < G; ++k)
 #pragma unroll
-          for (int e = 0; e < W; ++e) col[ty - 1][(k * W + e) * TX + tx] = acc[k][e];
+          for (int e = 0; e < W; ++e) col[((ty - 1) * G * W + k * W + e) * TX + tx] = acc[k][e];
       }
       __syncthreads();
     }
@@ -212,7 +275,7 @@ __global__ void __launch_bounds__(256) k_layernorm_bwd(const X* __restrict__ x, 
         for (int e = 0; e < W; ++e) {
           float s = acc[k][e];
 #pragma unroll
-          for (int i = 0; i < RY - 1; ++i) s += col[i][(k * W + e) * TX + tx];
+          for (int i = 0; i < RY - 1; ++i) s += col[(i * G * W + k * W + e) * TX + tx];
           if (c + e < d) out[which * d + c + e] = s;
         }
       }
@@ -244,10 +307,14 @@ __global__ void __launch_bounds__(1024) k_column_sums(const float* __restrict__ 
   }
 }
 
-// Blocks of the backward: two to each of 148 SMs, which its registers allow.
-constexpr int kLnMaxBlocks = 296;
+// The backward's blocks: as many as run at once on 148 SMs, fewer where a block
+// would have less than two row groups. Two to an SM bounds the scratch.
+constexpr int kLnMaxBlocks = 2 * 148;
 
-int ln_bwd_blocks(int T) { return T < kLnMaxBlocks ? (T > 0 ? T : 1) : kLnMaxBlocks; }
+int ln_bwd_blocks(int T, int per_sm, int ry) {
+  const int64_t most = ((int64_t)T + 2 * ry - 1) / (2 * ry);
+  return (int)(most < per_sm * 148 ? most : per_sm * 148);
+}
 
 template <typename X, typename Y, int TX, int G>
 int ln_fwd_launch(const void* x, int64_t ldx, const void* g, const void* b, void* y, int64_t ldy, float* mean,
@@ -276,11 +343,21 @@ int ln_fwd(const void* x, int64_t ldx, const void* g, const void* b, void* y, in
 
 template <typename X, typename Y, int TX, int G>
 int ln_bwd_launch(const LayerNormBwd& a, cudaStream_t st) {
-  const int nb = ln_bwd_blocks(a.T);
+  using L = LnBwd<X, Y, TX, G>;
+  const int nb = ln_bwd_blocks(a.T, L::PER_SM, L::RY);
   const int rpb = (a.T + nb - 1) / nb;
-  auto k = a.d % piece<X, Y>() ? k_layernorm_bwd<X, Y, TX, G, false> : k_layernorm_bwd<X, Y, TX, G, true>;
-  k<<<nb, 256, 0, st>>>((const X*)a.x, a.ldx, (const bf16*)a.g, a.mean, a.rstd, (const Y*)a.dy, a.lddy, (const X*)a.dres,
-                        a.lddres, (X*)a.dx, (bf16*)a.dx_bf16, a.lddx, a.part, a.T, a.d, rpb);
+  auto k = a.d % L::W ? k_layernorm_bwd<X, Y, TX, G, false> : k_layernorm_bwd<X, Y, TX, G, true>;
+  // Above 48 KB a kernel has to be told, once on each device.
+  static bool told[2][kMaxDevices] = {};
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess || device >= kMaxDevices) return MT_ERR_CUDA;
+  bool& is = told[a.d % L::W ? 1 : 0][device];
+  if (!is && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM) != cudaSuccess)
+    return MT_ERR_CUDA;
+  is = true;
+  k<<<nb, L::THREADS, L::SMEM, st>>>((const X*)a.x, a.ldx, (const bf16*)a.g, a.mean, a.rstd, (const Y*)a.dy, a.lddy,
+                                     (const X*)a.dres, a.lddres, (X*)a.dx, (bf16*)a.dx_bf16, a.lddx, a.part, a.T, a.d,
+                                     rpb);
   if (const int rc = launch_status()) return rc;
   return launch_column_sums(a.part, nb, 2 * (int64_t)a.d, 2 * a.d, a.dg, a.d, a.db, st);
 }
@@ -292,9 +369,9 @@ int ln_bwd(const LayerNormBwd& a, cudaStream_t st) {
   if (a.d <= 512) return ln_bwd_launch<X, Y, 64, P>(a, st);
   if (a.d <= 1024) return ln_bwd_launch<X, Y, 128, P>(a, st);
   if (a.d <= 2048) return ln_bwd_launch<X, Y, 256, P>(a, st);
-  if (a.d <= 4096) return ln_bwd_launch<X, Y, 256, 2 * P>(a, st);
-  if (a.d <= 6144) return ln_bwd_launch<X, Y, 256, 3 * P>(a, st);
-  return ln_bwd_launch<X, Y, 256, 4 * P>(a, st);
+  if (a.d <= 4096) return ln_bwd_launch<X, Y, 512, P>(a, st);
+  if (P == 2 && a.d <= 6144) return ln_bwd_launch<X, Y, 512, P + P / 2>(a, st);
+  return ln_bwd_launch<X, Y, 512, 2 * P>(a, st);
 }
 
 }  // namespace
@@ -315,7 +392,7 @@ int launch_layernorm_fwd(const void* x, int x_type, int64_t ldx, const void* g, 
   return ln_fwd<bf16, bf16>(x, ldx, g, b, y, ldy, mean, rstd, T, d, eps, st);
 }
 
-size_t layernorm_bwd_partial_floats(int T, int d) { return (size_t)ln_bwd_blocks(T) * 2 * d; }
+size_t layernorm_bwd_partial_floats(int T, int d) { return (size_t)(T < kLnMaxBlocks ? T + 1 : kLnMaxBlocks) * 2 * d; }
 
 int launch_layernorm_bwd(const LayerNormBwd& a, cudaStream_t st) {
   if (a.T <= 0) {  // sums over no rows

@@ -781,8 +781,6 @@ __global__ void __launch_bounds__(THREADS, 1)
 // ---------------------------------------------------------------------------
 // Host side.
 // ---------------------------------------------------------------------------
-constexpr int kMaxDevices = 64;
-
 // What a launch needs: operands and the tile-independent parameters.
 struct Op {
   const void* A;

@@ -111,10 +111,13 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* m, uin
 }
 
 // ---------------------------------------------------------------------------
-// Asynchronous 16-byte copies of a thread into shared memory, in groups.
+// Asynchronous copies of a thread into shared memory, in groups.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void copy16(uint32_t dst_smem, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst_smem), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst_smem, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst_smem), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Until at most N of the thread's latest groups are still in flight.
