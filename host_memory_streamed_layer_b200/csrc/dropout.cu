@@ -120,6 +120,7 @@ __global__ void __launch_bounds__(256, 4) k_act_bwd(const X* dc, int64_t lddc, c
                                                  const DropDesc drop, bf16* dz, int64_t lddz, float* __restrict__ part,
                                                  int M, int N, int rows_per_block, int tx_log2) {
   __shared__ float sh[256 * W];
+  let_next_start();  // every block of this kernel is resident from the start
   const int TX = 1 << tx_log2, tx = threadIdx.x & (TX - 1), ty = threadIdx.x >> tx_log2, ry = 256 >> tx_log2;
   const int c = (((int)blockIdx.x << tx_log2) + tx) * W;
   const int n = N - c;

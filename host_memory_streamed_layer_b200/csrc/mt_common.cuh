@@ -127,6 +127,15 @@ __device__ __forceinline__ void copy_wait() {
 }
 
 // ---------------------------------------------------------------------------
+// Programmatic dependent launch: a kernel launched with the attribute may
+// start once every block of the one before it has said so (or ended); it reads
+// nothing of that one before its wait, which lasts until that one has ended and
+// its writes are visible.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// ---------------------------------------------------------------------------
 // tcgen05: tensor memory allocation, MMA, commit, loads.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void tmem_alloc(uint32_t* dst_smem, uint32_t ncols) {
