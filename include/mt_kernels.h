@@ -180,7 +180,9 @@ int mt_k_gemm_bf16_rope(const void* A, int64_t lda, const void* B, int64_t ldb, 
  *     pitch is a multiple of 4 (fp32) or 8 (bf16) elements. Widths may be odd:
  *     nothing behind a row's last element is read or written;
  *   - all sums, statistics and activations are fp32; a bf16 output is rounded
- *     once, to nearest even, from the fp32 result;
+ *     once, to nearest even, from the fp32 result. A product of depth K is
+ *     accumulated by the tensor cores, which truncate: as in mt_k_gemm_bf16 it
+ *     comes out low by about 1.1e-9 K of itself;
  *   - the calls are deterministic: the same inputs give the same bits;
  *   - buffers may not overlap unless a call allows it; scratch belongs to one
  *     call in flight at a time (calls that may run at once, captured graphs
@@ -321,7 +323,8 @@ int mt_k_gated_ffn_bwd(const void* dy, int64_t lddy, const void* Wd, int64_t ldw
 
 /* Limit, in nanoseconds, of each main-loop wait of the single-CTA GEMM kernel
  * for later launches in this process (mt_k_gemm_bf16, mt_k_gemm_bf16_rope and
- * the engine's GEMMs alike); returns the previous limit. ns < 0 only queries.
+ * the engine's GEMMs alike, and the single-CTA tiles of mt_k_linear_* and
+ * mt_k_gated_ffn_*); returns the previous limit. ns < 0 only queries.
  * Default 1e9 (1 s). With 0 a wait gives up at its first poll that finds the
  * stage or accumulator not ready, so a test can make a kernel take its
  * bounded-wait exit without any fault: the kernel records an
@@ -336,7 +339,8 @@ int64_t mt_k_gemm_wait_limit_ns(int64_t ns);
 /* Selects the GEMM kernel family for later calls in this process: 0 automatic
  * (the default, or MT_GEMM_VARIANT=auto), 1 single-CTA tiles only (=single),
  * 2 CTA-pair tiles (tcgen05 cta_group::2, 256-row tiles) wherever a problem
- * has at least one pair tile per SM pair (=pair). Both families compute the
+ * has at least one pair tile per SM pair (=pair; the products with an epilogue,
+ * mt_k_linear_* and mt_k_gated_ffn_*, then always). Both families compute the
  * same product; this exists for measurement and tests. Returns the previous
  * family, or MT_ERR_ARG for another value (nothing changes). No GPU work. */
 int mt_k_gemm_variant(int variant);
