@@ -4,6 +4,7 @@
     python -m host_memory_streamed_layer_b200.kernel_bench attn [--fwd-only] [--iters N] [--attn-shape B,S,H[,HD]]
     python -m host_memory_streamed_layer_b200.kernel_bench rmsnorm_bwd [--iters N]
     python -m host_memory_streamed_layer_b200.kernel_bench elementwise [--iters N]
+    python -m host_memory_streamed_layer_b200.kernel_bench block [--iters N]
 
 Times each launch with CUDA events on the launching stream after warm-up and
 prints achieved TFLOP/s (tensor-bound kernels) or GB/s of algorithmic bytes
@@ -205,9 +206,64 @@ def bench_elementwise(iters, warmup):
     return out
 
 
+def bench_block(iters, warmup):
+    """Layer norm, dropout, the linear layers with an epilogue and the gated
+    feed-forward part at the 1.3B shape, each against its algorithmic FLOPs
+    (products) or bytes (the rest)."""
+    st = torch.cuda.current_stream().cuda_stream
+    dev, bf = "cuda", torch.bfloat16
+    P = lambda t: t.data_ptr()  # noqa: E731
+    out = []
+
+    def rec(name, fn, nbytes=0.0, flops=0.0):
+        sec = timed(fn, iters, warmup)
+        r = {"kernel": name, "us": sec * 1e6}
+        if sec:
+            r["tflops" if flops else "gbs"] = flops / sec / 1e12 if flops else nbytes / sec / 1e9
+        out.append(r)
+
+    x, dy, res, dx = (torch.randn(T, D, device=dev) for _ in range(4))
+    g, b = torch.ones(D, device=dev, dtype=bf), torch.zeros(D, device=dev, dtype=bf)
+    y, mean, rstd = torch.empty(T, D, device=dev, dtype=bf), torch.zeros(T, device=dev), torch.ones(T, device=dev)
+    rec("layernorm_fwd", lambda: mt.mt_k_layernorm_fwd(P(x), mt.MT_F32, D, P(g), P(b), P(y), mt.MT_BF16, D, P(mean),
+                                                       P(rstd), T, D, 1e-5, st), T * D * 6.0)
+    part = torch.empty(mt.mt_k_layernorm_bwd_partial_floats(T, D), device=dev)
+    dg, db = torch.empty(D, device=dev), torch.empty(D, device=dev)
+    rec("layernorm_bwd", lambda: mt.mt_k_layernorm_bwd(P(x), mt.MT_F32, D, P(g), P(mean), P(rstd), P(dy), mt.MT_F32, D,
+                                                       P(res), D, P(dx), P(y), D, P(part), P(dg), P(db), T, D, st),
+        T * D * 18.0)
+    drop = mt.mt_dropout(0.1, 1, 2)
+    rec("dropout + residual", lambda: mt.mt_k_dropout(P(y), mt.MT_BF16, D, drop, P(res), D, P(dx), mt.MT_F32, D, T, D,
+                                                      st), T * D * 10.0)
+    part = torch.empty(mt.mt_k_act_bwd_partial_floats(T, D), device=dev)
+    rec("act_bwd (dropout, bias gradient)", lambda: mt.mt_k_act_bwd(P(dy), mt.MT_F32, D, 0, 0, mt.MT_ACT_NONE, drop, P(y),
+                                                                    D, P(part), P(db), T, D, st), T * D * 6.0)
+    del dy, res
+    W1, W2 = torch.randn(F, D, device=dev).to(bf), torch.randn(D, F, device=dev).to(bf)
+    b1, Z, h = torch.zeros(F, device=dev, dtype=bf), torch.empty(T, F, device=dev, dtype=bf), \
+        torch.empty(T, F, device=dev, dtype=bf)
+    fl = 2.0 * T * F * D
+    rec("linear (bias, GELU, Z kept)", lambda: mt.mt_k_linear_fwd(P(y), D, P(W1), D, P(b1), mt.MT_ACT_GELU, None, 0, 0,
+                                                                  P(Z), F, P(h), mt.MT_BF16, F, T, F, D, st), flops=fl)
+    rec("linear (bias, dropout, residual)", lambda: mt.mt_k_linear_fwd(P(h), F, P(W2), F, P(b), mt.MT_ACT_NONE, drop,
+                                                                       P(x), D, 0, 0, P(dx), mt.MT_F32, D, T, D, F, st),
+        flops=fl)
+    part, db1 = torch.empty(mt.mt_k_linear_bwd_act_partial_floats(T, F), device=dev), torch.empty(F, device=dev)
+    rec("linear_bwd_act (GELU, bias gradient)",
+        lambda: mt.mt_k_linear_bwd_act(P(y), D, P(W2), F, P(Z), F, mt.MT_ACT_GELU, None, P(h), F, P(part), P(db1), T, F, D,
+                                       st), flops=fl)
+    Wgu, gu, dgu = (torch.randn(n, m, device=dev).to(bf) for n, m in ((2 * F, D), (T, 2 * F), (T, 2 * F)))
+    rec("gated_ffn_fwd (SiLU, gate and up kept)",
+        lambda: mt.mt_k_gated_ffn_fwd(P(y), D, P(Wgu), D, mt.MT_ACT_SILU, P(gu), 2 * F, P(h), F, T, F, D, st),
+        flops=2 * fl)
+    rec("gated_ffn_bwd (SiLU)", lambda: mt.mt_k_gated_ffn_bwd(P(y), D, P(W2), F, P(gu), 2 * F, mt.MT_ACT_SILU, P(dgu),
+                                                              2 * F, P(h), F, T, F, D, st), flops=fl)
+    return out
+
+
 def main():
     ap = argparse.ArgumentParser()
-    ap.add_argument("kernel", choices=["gemm", "attn", "rmsnorm_bwd", "elementwise"])
+    ap.add_argument("kernel", choices=["gemm", "attn", "rmsnorm_bwd", "elementwise", "block"])
     ap.add_argument("--shape", default="all")
     ap.add_argument("--iters", type=int, default=20)
     ap.add_argument("--warmup", type=int, default=3)
@@ -241,6 +297,8 @@ def main():
             r["shape"] = dict(b=ab, s=as_, heads=ah, hd=ahd)
     elif a.kernel == "elementwise":
         res = bench_elementwise(a.iters, a.warmup)
+    elif a.kernel == "block":
+        res = bench_block(a.iters, a.warmup)
     else:
         res = bench_rmsnorm_bwd(a.iters, a.warmup)
     for r in res:
