@@ -237,9 +237,10 @@ _sig("mt_k_gated_ffn_bwd", c_int, c_void_p, c_i64, c_void_p, c_i64, c_void_p, c_
      c_void_p, c_i64, c_int, c_int, c_int, c_void_p, c_void_p)
 
 
+# Pointers are integers here, 0 (or None) for NULL, as ctypes takes them.
 def mt_k_layernorm_fwd(x, x_type, ldx, g, b, y, y_type, ldy, mean, rstd, T, d, eps, stream=0):
-    return _check(lib.mt_k_layernorm_fwd(_p(x), x_type, ldx, _p(g), _p(b), _p(y), y_type, ldy, _p(mean), _p(rstd), T,
-                                         d, eps, _p(stream)), "mt_k_layernorm_fwd")
+    return _check(lib.mt_k_layernorm_fwd(x, x_type, ldx, g, b, y, y_type, ldy, mean, rstd, T,
+                                         d, eps, stream), "mt_k_layernorm_fwd")
 
 
 def mt_k_layernorm_bwd_partial_floats(T, d):
@@ -248,21 +249,21 @@ def mt_k_layernorm_bwd_partial_floats(T, d):
 
 def mt_k_layernorm_bwd(x, x_type, ldx, g, mean, rstd, dy, dy_type, lddy, dres, lddres, dx, dx_bf16, lddx, part, dg,
                        db, T, d, stream=0):
-    return _check(lib.mt_k_layernorm_bwd(_p(x), x_type, ldx, _p(g), _p(mean), _p(rstd), _p(dy), dy_type, lddy,
-                                         _p(dres), lddres, _p(dx), _p(dx_bf16), lddx, _p(part), _p(dg), _p(db), T, d,
-                                         _p(stream)), "mt_k_layernorm_bwd")
+    return _check(lib.mt_k_layernorm_bwd(x, x_type, ldx, g, mean, rstd, dy, dy_type, lddy,
+                                         dres, lddres, dx, dx_bf16, lddx, part, dg, db, T, d,
+                                         stream), "mt_k_layernorm_bwd")
 
 
 def mt_k_dropout(x, x_type, ldx, drop, res, ldr, y, y_type, ldy, T, d, stream=0):
     """drop: an mt_dropout or None."""
-    return _check(lib.mt_k_dropout(_p(x), x_type, ldx, drop, _p(res), ldr, _p(y), y_type, ldy, T, d, _p(stream)),
+    return _check(lib.mt_k_dropout(x, x_type, ldx, drop, res, ldr, y, y_type, ldy, T, d, stream),
                   "mt_k_dropout")
 
 
 def mt_k_linear_fwd(A, lda, W, ldw, bias, act, drop, R, ldr, Z, ldz, C, out_type, ldc, M, N, K, stream=0, dev_err=0):
     """drop: an mt_dropout or None."""
-    return _check(lib.mt_k_linear_fwd(_p(A), lda, _p(W), ldw, _p(bias), act, drop, _p(R), ldr, _p(Z), ldz, _p(C),
-                                      out_type, ldc, M, N, K, _p(stream), _p(dev_err)), "mt_k_linear_fwd")
+    return _check(lib.mt_k_linear_fwd(A, lda, W, ldw, bias, act, drop, R, ldr, Z, ldz, C,
+                                      out_type, ldc, M, N, K, stream, dev_err), "mt_k_linear_fwd")
 
 
 def mt_k_linear_bwd_act_partial_floats(M, N):
@@ -271,8 +272,8 @@ def mt_k_linear_bwd_act_partial_floats(M, N):
 
 def mt_k_linear_bwd_act(dY, lddy, W, ldw, Z, ldz, act, drop, dZ, lddz, part, db, M, N, K, stream=0, dev_err=0):
     """drop: an mt_dropout or None."""
-    return _check(lib.mt_k_linear_bwd_act(_p(dY), lddy, _p(W), ldw, _p(Z), ldz, act, drop, _p(dZ), lddz, _p(part),
-                                          _p(db), M, N, K, _p(stream), _p(dev_err)), "mt_k_linear_bwd_act")
+    return _check(lib.mt_k_linear_bwd_act(dY, lddy, W, ldw, Z, ldz, act, drop, dZ, lddz, part,
+                                          db, M, N, K, stream, dev_err), "mt_k_linear_bwd_act")
 
 
 def mt_k_act_bwd_partial_floats(M, N):
@@ -281,18 +282,18 @@ def mt_k_act_bwd_partial_floats(M, N):
 
 def mt_k_act_bwd(dC, dc_type, lddc, Z, ldz, act, drop, dZ, lddz, part, db, M, N, stream=0):
     """drop: an mt_dropout or None."""
-    return _check(lib.mt_k_act_bwd(_p(dC), dc_type, lddc, _p(Z), ldz, act, drop, _p(dZ), lddz, _p(part), _p(db), M, N,
-                                   _p(stream)), "mt_k_act_bwd")
+    return _check(lib.mt_k_act_bwd(dC, dc_type, lddc, Z, ldz, act, drop, dZ, lddz, part, db, M, N,
+                                   stream), "mt_k_act_bwd")
 
 
 def mt_k_gated_ffn_fwd(x, ldx, Wgu, ldw, act, gu, ldgu, h, ldh, M, F, K, stream=0, dev_err=0):
-    return _check(lib.mt_k_gated_ffn_fwd(_p(x), ldx, _p(Wgu), ldw, act, _p(gu), ldgu, _p(h), ldh, M, F, K,
-                                         _p(stream), _p(dev_err)), "mt_k_gated_ffn_fwd")
+    return _check(lib.mt_k_gated_ffn_fwd(x, ldx, Wgu, ldw, act, gu, ldgu, h, ldh, M, F, K,
+                                         stream, dev_err), "mt_k_gated_ffn_fwd")
 
 
 def mt_k_gated_ffn_bwd(dy, lddy, Wd, ldw, gu, ldgu, act, dgu, lddgu, h, ldh, M, F, K, stream=0, dev_err=0):
-    return _check(lib.mt_k_gated_ffn_bwd(_p(dy), lddy, _p(Wd), ldw, _p(gu), ldgu, act, _p(dgu), lddgu, _p(h), ldh, M,
-                                         F, K, _p(stream), _p(dev_err)), "mt_k_gated_ffn_bwd")
+    return _check(lib.mt_k_gated_ffn_bwd(dy, lddy, Wd, ldw, gu, ldgu, act, dgu, lddgu, h, ldh, M,
+                                         F, K, stream, dev_err), "mt_k_gated_ffn_bwd")
 
 
 # ---------------------------------------------------------------------------

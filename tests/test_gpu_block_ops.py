@@ -120,9 +120,9 @@ def test_layernorm_fwd(T, d, xt, yt):
         x.np()  # untouched padding
 
 
-def test_layernorm_fwd_without_statistics_in_place_and_bad_rows():
-    """mean and rstd are optional; y may take x's place; a row with a NaN or an
-    infinity spoils itself only; a constant row gives b."""
+def test_layernorm_fwd_without_statistics_and_bad_rows():
+    """mean and rstd are optional; a row with a NaN or an infinity spoils itself
+    only; a constant row gives b."""
     mt = _mt()
     T, d = 40, 515
     _, x, g, b = ln_inputs(T, d, torch.float32, torch.float32)
@@ -617,6 +617,77 @@ def test_bounded_wait_ends_the_call_and_the_next_one_is_right():
     assert int(err) == 0
     a, w = np64(A), np64(W)
     within(np64(C), a @ w.T, product_error(a, w, K) + 2.0 ** -24 * np.abs(a @ w.T))
+
+
+@pytest.mark.parametrize("out", TYPES)
+@pytest.mark.parametrize("M,N,K", [(1, 40, 24), (300, 200, 100), (1290, 1100, 200)])
+def test_in_place_calls_give_the_bits_of_separate_buffers(M, N, K, out):
+    """C over R, dZ over Z, dZ over a bf16 dC, dx over dres: what the header
+    allows gives the same bits as buffers of their own."""
+    mt = _mt()
+    rng = np.random.default_rng(M + N)
+    A, W = Mat(M, K, torch.bfloat16, rng.normal(size=(M, K))), Mat(N, K, torch.bfloat16, rng.normal(size=(N, K)))
+    r, z = rng.normal(size=(M, N)), rng.normal(size=(M, N))
+    drop = mt.mt_dropout(0.25, SEED, OFFSET)
+    got = []
+    for inplace in (False, True):
+        R = Mat(M, N, out, r)
+        C = R if inplace else Mat(M, N, out)
+        mt.mt_k_linear_fwd(A.ptr, A.ld, W.ptr, W.ld, 0, mt.MT_ACT_SILU, drop, R.ptr, R.ld, 0, 0, C.ptr, C.kind, C.ld, M, N, K,
+                           stream())
+        Z, dC = Mat(M, N, torch.bfloat16, z), Mat(M, N, out, r)
+        dZ = Z if inplace else Mat(M, N, torch.bfloat16)
+        db = scratch(N)
+        mt.mt_k_act_bwd(dC.ptr, dC.kind, dC.ld, Z.ptr, Z.ld, mt.MT_ACT_GELU, drop, dZ.ptr, dZ.ld,
+                        scratch(mt.mt_k_act_bwd_partial_floats(M, N)).data_ptr(), db.data_ptr(), M, N, stream())
+        got.append([C.np(), dZ.np(), np64(db)[:N]])
+        if out == torch.bfloat16:
+            Z, dC = Mat(M, N, torch.bfloat16, z), Mat(M, N, out, r)
+            dZ = dC if inplace else Mat(M, N, torch.bfloat16)
+            mt.mt_k_act_bwd(dC.ptr, dC.kind, dC.ld, Z.ptr, Z.ld, mt.MT_ACT_RELU, drop, dZ.ptr, dZ.ld, 0, 0, M, N, stream())
+            got[-1].append(dZ.np())
+    assert all(np.array_equal(a, b) for a, b in zip(*got))
+
+
+@pytest.mark.late
+def test_gated_and_backward_offsets_past_31_bits():
+    """gu, dgu, Z and dZ of more than 2^31 elements: rows at both ends are right."""
+    mt = _mt()
+    F, K = 4096, 16
+    M = (1 << 31) // F + 777
+    g = torch.Generator(device=DEV).manual_seed(5)
+    at = [0, 3, M - 700, M - 1]
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device=DEV)
+    x[at] = torch.randn(len(at), K, generator=g, device=DEV).bfloat16()
+    W, Wd = torch.randn(2 * F, K, generator=g, device=DEV).bfloat16(), torch.randn(K, F, generator=g, device=DEV).bfloat16()
+    gu, h = torch.empty(M, 2 * F, dtype=torch.bfloat16, device=DEV), torch.empty(M, F, dtype=torch.bfloat16, device=DEV)
+    mt.mt_k_gated_ffn_fwd(x.data_ptr(), K, W.data_ptr(), K, mt.MT_ACT_SILU, gu.data_ptr(), 2 * F, h.data_ptr(), F, M, F, K, stream())
+    X, WW = np64(x[at]), np64(W)
+    want, gate, up = block.gated_fwd(X, WW[:F], WW[F:], "silu")
+    e = product_error(X, WW, K)
+    both = np.concatenate([gate, up], axis=1)
+    within(np64(gu[at]), both, 2.0 ** -8 * np.abs(both) + e)
+    ea, eu = 1.13 * e[:, :F] + 2.0 ** -20 * np.abs(gate), e[:, F:]
+    within(np64(h[at]), want, (2.0 ** -8 + 2.0 ** -22) * np.abs(want) + ea * np.abs(up) + (np.abs(block.act(gate, "silu")) + ea) * eu)
+    assert not gu[M - 699:M - 1].any() and not h[M - 699:M - 1].any()
+    # back, over gu itself, and through a linear layer over Z itself
+    GU = np64(gu[at])
+    mt.mt_k_gated_ffn_bwd(x.data_ptr(), K, Wd.data_ptr(), F, gu.data_ptr(), 2 * F, mt.MT_ACT_SILU, gu.data_ptr(), 2 * F, 0, 0, M, F,
+                          K, stream())
+    wg, wu, _ = block.gated_bwd(X, np64(Wd), GU[:, :F], GU[:, F:], "silu")
+    dh, ed = X @ np64(Wd), product_error(X, np64(Wd).T, K)
+    tol = np.concatenate([np.abs(GU[:, F:]) * (1.13 * ed + 2.0 ** -20 * (1 + np.abs(GU[:, :F])) * np.abs(dh)),
+                          np.abs(block.act(GU[:, :F], "silu")) * ed + 2.0 ** -20 * np.abs(GU[:, :F]) * np.abs(dh)], axis=1)
+    want = np.concatenate([wg, wu], axis=1)
+    within(np64(gu[at]), want, (2.0 ** -8 + 2.0 ** -22) * np.abs(want) + tol)
+    Z = np64(h[at])
+    part, db = scratch(mt.mt_k_linear_bwd_act_partial_floats(M, F)), scratch(F)
+    mt.mt_k_linear_bwd_act(x.data_ptr(), K, Wd.data_ptr(), F, h.data_ptr(), F, mt.MT_ACT_GELU, None, h.data_ptr(), F, part.data_ptr(),
+                           db.data_ptr(), M, F, K, stream())
+    want, wdb = block.linear_bwd_act(X, np64(Wd), Z, "gelu")
+    e = 1.13 * ed + 2.0 ** -20 * (1 + np.abs(Z)) * np.abs(dh)
+    within(np64(h[at]), want, 2.0 ** -8 * np.abs(want) + e)
+    within(np64(db)[:F], wdb, e.sum(axis=0) + CHAIN * np.abs(want).sum(axis=0))  # the other rows' dY is zero
 
 
 @pytest.mark.late
