@@ -77,6 +77,10 @@ struct Ahead {
 // a time.
 struct Tile {
   int bn, a_rows, b_rows, sub, stages;
+  // The full-width pair kernel only: the first `whole` tiles fill whole waves;
+  // each of the rest is cut into `split` narrower ones (1, 2 or 4), so that the
+  // last wave is shared by more pairs.
+  int whole, split;
 };
 
 struct Params {
@@ -432,7 +436,8 @@ __device__ __forceinline__ bool wait_or_look(uint32_t bar, uint32_t parity, uint
 template <bool PAIR, int EPI, bool WIDE>
 __global__ void __launch_bounds__(THREADS, 1)
     k_linear(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-             const __grid_constant__ CUtensorMap tmB2, const __grid_constant__ Params p) {
+             const __grid_constant__ CUtensorMap tmB2, const __grid_constant__ CUtensorMap tmS,
+             const __grid_constant__ CUtensorMap tmS2, const __grid_constant__ Params p) {
   constexpr bool GATED = EPI == E_GATED;
   constexpr bool B_MN = EPI == E_BWD || EPI == E_GATED_BWD;  // B is stored [K, N]
   constexpr int TILE_M = PAIR ? 2 * BM : BM;
@@ -494,7 +499,17 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   const int num_m = (p.M + TILE_M - 1) / TILE_M;
   const int num_n = (p.N + on - 1) / on;
-  const int num_tiles = num_m * num_n;
+  const int whole = WIDE ? p.t.whole : num_m * num_n, split = WIDE ? p.t.split : 1;
+  const int num_tiles = whole + (num_m * num_n - whole) * split;
+  // Tile index -> row block, first output column and output columns of the tile.
+  auto tile_at = [&](int tile, int& mb, int& first, int& width) {
+    const bool cut = WIDE && tile >= whole;
+    const int u = tile - whole;
+    int nb;
+    tile_coords(cut ? whole + u / split : tile, num_m, num_n, mb, nb);
+    width = cut ? on / split : on;
+    first = nb * on + (cut ? u % split * width : 0);
+  };
   const int num_kb = (p.K + BK - 1) / BK;
   const int first_tile = PAIR ? blockIdx.x >> 1 : blockIdx.x;
   const int tile_step = PAIR ? gridDim.x >> 1 : gridDim.x;
@@ -508,12 +523,15 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t empty0 = smem_u32(&empty[0]);
     bool ok = true;
     for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
-      int mb, nb;
-      tile_coords(tile, num_m, num_n, mb, nb);
+      int mb, first, width;
+      tile_at(tile, mb, first, width);
       const int m0 = mb * TILE_M + (int)rank * BM;
       // A pair's B rows are split over its CTAs; a gated tile has one half from each weight.
-      const int n0 = nb * on + (PAIR && !GATED ? (int)rank * (bn / 2) : 0);
-      const CUtensorMap* mB = PAIR && GATED && rank ? &tmB2 : &tmB;
+      const int n0 = first + (PAIR && !GATED ? (int)rank * (width / 2) : 0);
+      const bool cut = WIDE && width < on;  // tmS, tmS2: the same weights by fewer rows
+      const CUtensorMap* mB = PAIR && GATED && rank ? (cut ? &tmS2 : &tmB2) : cut ? &tmS : &tmB;
+      const int rows = cut ? b_rows / split : b_rows;
+      const uint32_t bytes = a_bytes + rows * (BK * 2);
       for (int kb = 0; kb < num_kb; kb += sub) {
         const bool got = wait_or_look(empty0 + 8 * stage, phase ^ 1, limit);
         if (!__all_sync(0xffffffffu, got && !*abort_flag)) {
@@ -525,7 +543,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         int k0 = kb * BK;
         if (elect_one()) {
           const uint32_t fb = fb0 + 8 * stage;
-          if (!PAIR || rank == 0) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * n * kb_bytes);
+          if (!PAIR || rank == 0) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * n * bytes);
           auto load = [&] {
             uint8_t* sb = sa + a_bytes;
             if (PAIR) {
@@ -534,7 +552,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tma_load_2d_pair(sb, mB, fb, k0, n0);
               } else {
                 tma_load_2d_pair(sb, mB, fb, n0, k0);
-                if (b_rows > 64) tma_load_2d_pair(sb + 8192, mB, fb, n0 + 64, k0);
+                if (rows > 64) tma_load_2d_pair(sb + 8192, mB, fb, n0 + 64, k0);
               }
             } else {
               tma_load_2d(sa, &tmA, &full[stage], k0, m0);
@@ -612,7 +630,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       // loop inside one lane's branch, every MMA and commit first moved its
       // operands to uniform registers, and a k-block took 560 cycles and more
       // to issue where the tensor core needs 512.
-      const uint32_t idesc = idesc_bf16_f32(TILE_M, bn, false, B_MN);
+      const uint32_t idesc_whole = idesc_bf16_f32(TILE_M, bn, false, B_MN);
+      const uint32_t idesc_cut = idesc_bf16_f32(TILE_M, bn / split, false, B_MN);
       // Descriptors of stage 0; stages and k-steps only move the start address.
       const uint32_t s0 = smem_u32(smem);
       const uint64_t a0 = sdesc_sw128(s0, 16, 1024);
@@ -635,6 +654,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * 256;
+        const uint32_t idesc = WIDE && tile >= whole ? idesc_cut : idesc_whole;
         for (int kb = 0; kb < num_kb; kb += sub) {
           if (!__all_sync(0xffffffffu, wait_or_look(full0 + 8 * stage, phase, limit))) {
             ok = false;
@@ -711,12 +731,14 @@ __global__ void __launch_bounds__(THREADS, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int tile = first_tile; tile < num_tiles; tile += tile_step) {
-      int mb, nb;
-      tile_coords(tile, num_m, num_n, mb, nb);
+      int mb, first, width;
+      tile_at(tile, mb, first, width);
       const int row0 = mb * TILE_M + (int)rank * BM + quarter * 32 + Lay<EPI>::row(lane);  // this lane's first row
-      const int end = min(p.N, (nb + 1) * on), all = (end - nb * on + 31) >> 5, first_half = (all + 1) >> 1;
-      const int blocks = half ? all - first_half : first_half;  // 0 in the second half of a tile of one block
-      const int share = half ? 32 * first_half : 0, col0 = nb * on + share;
+      // The warp's blocks; none (or less) in the second half of a tile of one
+      // block and in a part of a tile that lies behind the last column.
+      const int end = min(p.N, first + width), all = (end - first + 31) >> 5, first_half = (all + 1) >> 1;
+      const int blocks = half ? all - first_half : first_half;
+      const int share = half ? 32 * first_half : 0, col0 = first + share;
       const bool full_rows = mb * TILE_M + (int)rank * BM + quarter * 32 + 32 <= p.M;
       auto inside = [&](int k) { return full_rows && col0 + 32 * k + 32 <= end; };
       // One group of copies to a block, empty where there is nothing to copy.
@@ -748,7 +770,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_arrive(&tempty[acc]);
         }
       };
-      if (blocks == 0) release();
+      if (blocks <= 0) release();
 #pragma unroll 1
       for (int k = 0; k < blocks; ++k) {
         const int col = col0 + 32 * k + Lay<EPI>::col(lane);  // this lane's first column
@@ -756,7 +778,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         tmem_ld_32x32b_x32(tbase + 32 * k, a);
         if (GATED) {
           uint32_t b[32];
-          tmem_ld_32x32b_x32(tbase + on + 32 * k, b);
+          tmem_ld_32x32b_x32(tbase + width + 32 * k, b);
           tmem_ld_wait();
           if (k == blocks - 1) release();
           MT_WITH_ACT(p.act, (gated_block<ACT>(p, row0, col, end, lane, reinterpret_cast<uint4*>(st), a, b)));
@@ -813,6 +835,33 @@ struct Op {
   int64_t ldb;
   Params p;
 };
+
+// A k-block's cost to an SM: the larger of its MMAs (2 bn cycles for 128 rows, or
+// for each half of a pair's 256) and of fetching its operands from L2 at about 60
+// bytes a cycle, which is what bounds narrow tiles: 128 x 128 takes 546 cycles for
+// 256 of MMA. In 60ths of a cycle.
+int block_cost(int a_rows, int b_rows, int bn) {
+  const int bytes = (a_rows + b_rows) * 128;
+  return 2 * bn * 60 > bytes ? 2 * bn * 60 : bytes;
+}
+
+// The last wave of full-width pair tiles, `rest` of them for n pairs: cut in 1, 2
+// or 4 (an MN-major operand comes in pieces of 64 columns: at most 2), whichever
+// costs least. Measured on one B200, interleaved: the gated backward of 4099 x
+// 1408 x 2048 (102 tiles: 74 whole, 28 cut in two) 38.1 us instead of 41.6, of
+// 2048 x 5504 x 2048 61.9 instead of 71.5.
+struct LastWave {
+  int split;
+  int64_t cost;
+};
+LastWave last_wave(int rest, int n, bool mn_major) {
+  LastWave best{1, INT64_MAX};
+  for (int s = 1; s <= (mn_major ? 2 : 4); s *= 2) {
+    const int64_t c = (int64_t)((rest * s + n - 1) / n) * block_cost(BM, 128 / s, 256 / s);
+    if (c < best.cost) best = LastWave{s, c};
+  }
+  return best;
+}
 
 template <bool PAIR, int EPI, bool WIDE>
 int launch(Op o, int bn, int device, int num_sms, cudaStream_t st) {
@@ -878,18 +927,28 @@ int launch(Op o, int bn, int device, int num_sms, cudaStream_t st) {
     }
     resident[device] = r;
   }
-  const int64_t tiles = (int64_t)((p.M + TILE_M - 1) / TILE_M) * ((p.N + on - 1) / on);
-  if (tiles > INT32_MAX / 2) return MT_ERR_ARG;
+  int64_t tiles = (int64_t)((p.M + TILE_M - 1) / TILE_M) * ((p.N + on - 1) / on);
+  if (tiles > INT32_MAX / 8) return MT_ERR_ARG;
+  p.t.whole = (int)tiles, p.t.split = 1;
+  CUtensorMap ts = tb, ts2 = tb2;
+  if (WIDE) {
+    const int rest = (int)(tiles % resident[device]);
+    p.t.split = tiles > rest ? last_wave(rest, resident[device], B_MN).split : 1;
+    if (p.t.split > 1) {
+      p.t.whole = (int)tiles - rest;
+      tiles = p.t.whole + (int64_t)rest * p.t.split;
+      if (!B_MN) ok = make_tensor_map_2d_bf16(&ts, o.B, p.K, p.N, o.ldb, p.t.b_rows / p.t.split);
+      if (GATED) ok = ok && make_tensor_map_2d_bf16(&ts2, o.B2, p.K, p.N, o.ldb, p.t.b_rows / p.t.split);
+      if (!ok) return MT_ERR_ARG;
+    }
+  }
   const int n = tiles < resident[device] ? (int)tiles : resident[device];
   cfg.gridDim = dim3(PAIR ? 2 * n : n, 1, 1);
-  cudaLaunchKernelEx(&cfg, kernel, ta, tb, tb2, p);
+  cudaLaunchKernelEx(&cfg, kernel, ta, tb, tb2, ts, ts2, p);
   return launch_status();
 }
 
-// The tile is the one whose waves cost least. A k-block costs an SM the larger
-// of its MMAs (2 bn cycles for 128 rows, or for each half of a pair's 256) and
-// of fetching its operands from L2 at about 60 bytes a cycle, which is what
-// bounds narrow tiles: 128 x 128 takes 546 cycles for 256 of MMA.
+// The tile is the one whose waves cost least by block_cost().
 template <int EPI>
 int dispatch(const Op& o, cudaStream_t st) {
   int device = 0, sms = 0;
@@ -910,8 +969,9 @@ int dispatch(const Op& o, cudaStream_t st) {
   auto consider = [&](int bn, bool pair) {
     const int tm = pair ? 2 * BM : BM, tn = bn / G, n = pair ? sms / 2 : sms;
     const int64_t tiles = ((int64_t)o.p.M + tm - 1) / tm * ((o.p.N + tn - 1) / tn);
-    const int bytes = (o.p.M < BM ? o.p.M : BM) * 128 + (pair ? bn / 2 : bn) * 128;
-    const int64_t cost = (tiles + n - 1) / n * (2 * bn * 60 > bytes ? 2 * bn * 60 : bytes);
+    const int each = block_cost(o.p.M < BM ? o.p.M : BM, pair ? bn / 2 : bn, bn);
+    const int64_t cost = pair && bn == 256 && tiles > n ? tiles / n * each + last_wave((int)(tiles % n), n, B_MN).cost
+                                                        : (tiles + n - 1) / n * each;
     // On a tie the wider tile, but single CTAs before pairs.
     if (cost < least || (cost == least && best_pair && !pair)) least = cost, best = bn, best_pair = pair;
   };

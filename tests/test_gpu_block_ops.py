@@ -552,6 +552,21 @@ def test_gated_activations(act):
     within(h.np(), want, (HALF[torch.bfloat16] + 2.0 ** -22) * np.abs(want) + ea * np.abs(u) + (np.abs(block.act(g, act)) + ea) * eu)
 
 
+@pytest.mark.parametrize("fam", [0, 2])
+@pytest.mark.parametrize("M,N,K", [(2309, 1948, 136), (2309, 2048, 64), (4000, 1300, 200), (19200, 264, 40)])
+def test_a_last_wave_of_narrower_tiles(M, N, K, fam):
+    """More 256-wide pair tiles than a 148-SM part has pairs, and some left over:
+    those are cut in two or four, with parts that end inside the matrix, at its
+    edge and behind it."""
+    with family(fam):
+        linear_case(M, N, K, "silu", torch.bfloat16, 0.1, True)
+        linear_case(M, N, K, "none", torch.float32, 0.0, True)
+        bwd_case(M, N, K, "gelu", 0.0)
+    F = (N // 2 + 7) // 8 * 8
+    test_gated_fwd(M, F, K, fam, "silu")
+    test_gated_bwd(M, (N + 7) // 8 * 8, K, fam, "silu")
+
+
 # ---------------------------------------------------------------------------
 # Calls beside one another
 # ---------------------------------------------------------------------------
