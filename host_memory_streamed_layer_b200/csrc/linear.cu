@@ -12,6 +12,7 @@
 //   warp 1      MMA issuer: one lane issues tcgen05.mma on 128 x bn x 16
 //               (256 x bn x 16 for a pair of CTAs)
 //   warps 2..9  epilogue: tcgen05.ld from tensor memory, elementwise, store
+//               (4..11 where sums are held in registers, see CHUNK_MOST)
 // The accumulator is double-buffered in tensor memory (2 x 256 columns), so the
 // epilogue of one tile runs under the main loop of the next.
 //
@@ -28,14 +29,6 @@
 // torch.matmul of the same product at 278 us: 270 us with a bias alone, 291 us
 // with GELU and the pre-activation kept, 300 us for the backward step with the
 // bias gradient; 8192 x 13824 x 5120 gated 1512 us (1534 TFLOP/s) beside 1638.
-//
-// Accuracy: the tensor core adds each step of 16 products to the fp32
-// accumulator by truncation, so a sum comes out low by about 1.1e-9 K of itself
-// (2e-6 at K = 2048, 6e-6 at 5504, measured, as for every product of this
-// library). Beside a bf16 output's rounding that is nothing; an fp32 C and db
-// carry it. Adding up every 896 products in registers instead gave 8e-7, but
-// its warps could not keep up with the tensor cores: the fp32 residual at
-// 16333 x 2048 x 5504 went from 290 to 364 us.
 #include <type_traits>
 
 #include "act_dropout.cuh"
@@ -56,7 +49,29 @@ enum Epi : int { E_LINEAR_BF16, E_LINEAR_F32, E_BWD, E_GATED, E_GATED_BWD };
 // Epilogue warps: two to a lane quarter, each taking one half of a tile's blocks
 // of 32 columns.
 constexpr int EPI_WARPS = 8;
-constexpr int THREADS = 64 + 32 * EPI_WARPS;
+
+// The tensor core adds a step of 16 products to its accumulator by truncation:
+// a sum comes out low by about 9.5e-10 K of itself. Beside a bf16 output's
+// rounding that is nothing, but fp32 outputs (a residual stream, the bias
+// gradient) would show it: 2e-6 at K = 2048, 6e-6 at 5504, where one in fp32
+// registers is off by under 1e-6. So from K = 960 on their kernels accumulate a
+// chunk of the k-blocks at a time and add the chunks in the epilogue warps'
+// registers (CHUNKED). Measured on one B200, interleaved, plain -> chunked: error
+// 6.0e-6 -> 8.6e-7 and 265 -> 293 us for dropout and an fp32 residual at 16333 x
+// 2048 x 5504; the bias gradient's 2.1e-6 -> 8.9e-7 and 286 -> 310 us at 16384 x
+// 5504 x 2048.
+constexpr int CHUNK_MOST = 14;  // k-blocks of a K that is accumulated at once
+constexpr bool may_chunk(int epi) { return epi == E_LINEAR_F32 || epi == E_BWD; }
+
+// Their 128 sums a thread do not fit the 168 registers of ten or twelve warps,
+// so the copy and MMA warps fill a warpgroup of four (two of them idle) that
+// gives registers to the eight epilogue warps: 56 x 128 + 224 x 256 = 168 x 384.
+template <bool CHUNKED>
+struct Warps {
+  static constexpr int FIRST = CHUNKED ? 4 : 2;  // the first epilogue warp
+  static constexpr int THREADS = 32 * (FIRST + EPI_WARPS);
+  static constexpr int FEW = 56, MANY = 224;
+};
 constexpr int SMEM_MOST = 232448;  // 227 KB
 constexpr int BAR_BYTES = 256;     // barriers of at most 12 stages
 constexpr int MAX_STAGES = 12;
@@ -81,6 +96,10 @@ struct Tile {
   // each of the rest is cut into `split` narrower ones (1, 2 or 4), so that the
   // last wave is shared by more pairs.
   int whole, split;
+  // k-blocks of an accumulation, multiples of sub: the first two chunks of a
+  // tile, which run while the epilogue warps finish the tile before, and the
+  // others.
+  int chunk_first, chunk_rest;
 };
 
 struct Params {
@@ -433,8 +452,8 @@ __device__ __forceinline__ bool wait_or_look(uint32_t bar, uint32_t parity, uint
 // the leader's `tempty`. tmB2 is Wu's map for a gated product and unused
 // otherwise.
 // ---------------------------------------------------------------------------
-template <bool PAIR, int EPI, bool WIDE>
-__global__ void __launch_bounds__(THREADS, 1)
+template <bool PAIR, int EPI, bool WIDE, bool CHUNKED>
+__global__ void __launch_bounds__(Warps<CHUNKED>::THREADS, 1)
     k_linear(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
              const __grid_constant__ CUtensorMap tmB2, const __grid_constant__ CUtensorMap tmS,
              const __grid_constant__ CUtensorMap tmS2, const __grid_constant__ Params p) {
@@ -511,9 +530,17 @@ __global__ void __launch_bounds__(THREADS, 1)
     first = nb * on + (cut ? u % split * width : 0);
   };
   const int num_kb = (p.K + BK - 1) / BK;
+  constexpr int FIRST = Warps<CHUNKED>::FIRST;
+  // The end of the chunk that begins at k-block kb0.
+  auto chunk_end = [&](int kb0) {
+    if (!CHUNKED) return num_kb;
+    return min(num_kb, kb0 + (kb0 <= p.t.chunk_first ? p.t.chunk_first : p.t.chunk_rest));
+  };
   const int first_tile = PAIR ? blockIdx.x >> 1 : blockIdx.x;
   const int tile_step = PAIR ? gridDim.x >> 1 : gridDim.x;
 
+  if (warp < FIRST) {
+  if (CHUNKED) lower_registers<Warps<CHUNKED>::FEW>();
   if (warp == 0) {
     // ---------------- TMA producer (the whole warp; one elected lane copies) ----------------
     int stage = 0;
@@ -645,7 +672,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       uint32_t acc_phase = 0;
       bool ok = true;
       bool issued = false;
-      for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
+      for (int tile = first_tile, kb0 = 0; tile < num_tiles && ok;) {
         const bool free_acc = PAIR ? mbar_wait_cluster(&tempty[acc], acc_phase ^ 1)
                                    : wait_or_look(smem_u32(&tempty[acc]), acc_phase ^ 1, limit);
         if (!__all_sync(0xffffffffu, free_acc && !*abort_flag)) {
@@ -655,7 +682,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * 256;
         const uint32_t idesc = WIDE && tile >= whole ? idesc_cut : idesc_whole;
-        for (int kb = 0; kb < num_kb; kb += sub) {
+        const int kb1 = chunk_end(kb0);
+        for (int kb = kb0; kb < kb1; kb += sub) {
           if (!__all_sync(0xffffffffu, wait_or_look(full0 + 8 * stage, phase, limit))) {
             ok = false;
             break;
@@ -663,7 +691,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           // The stage's bytes were written by TMA and published through this
           // mbarrier, which orders them for the MMAs' reads: no tcgen05 fence.
           uint64_t ad = a0 + stage * kStage, bd = b0 + stage * kStage;
-          const int n = min(sub, num_kb - kb);
+          const int n = min(sub, kb1 - kb);
           if (elect_one()) {
             auto multiply = [&](bool accumulate) {
 #pragma unroll
@@ -674,7 +702,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                   umma_bf16(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, accumulate || kk != 0);
               }
             };
-            multiply(kb != 0);
+            multiply(kb != kb0);
 #pragma unroll 1
             for (int i = 1; i < n; ++i) {
               ad += kBlock, bd += kBlock;
@@ -684,7 +712,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               umma_commit_both(empty0 + 8 * stage);
             else
               umma_commit_u32(empty0 + 8 * stage);
-            if (kb + n == num_kb) {
+            if (kb + n == kb1) {
               if (PAIR)
                 umma_commit_both(tfull0 + 8 * acc);
               else
@@ -702,6 +730,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           acc = 0;
           acc_phase ^= 1;
         }
+        kb0 = kb1;
+        if (kb1 == num_kb) kb0 = 0, tile += tile_step;
       }
       if (!ok && lane == 0) {
         record_error(p.err, DEV_TIMEOUT_MMA);
@@ -720,13 +750,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (!mbar_wait(drain, 0) && lane == 0) record_error(p.err, DEV_TIMEOUT_TEARDOWN);
       }
     }
+  }
   } else {
+    if (CHUNKED) raise_registers<Warps<CHUNKED>::MANY>();
     // ---------------- epilogue ----------------
     const int quarter = warp & 3;                // tensor-memory lanes this warp may read
-    const int half = (warp - 2) >> 2;            // takes the first or the second half of the tile's blocks
+    const int half = (warp - FIRST) >> 2;            // takes the first or the second half of the tile's blocks
     uint8_t* mine = smem + stages * stage_bytes + BAR_BYTES;
-    float* st = reinterpret_cast<float*>(mine + (warp - 2) * EPI_BYTES);
-    const uint4* fetched = reinterpret_cast<uint4*>(mine + EPI_WARPS * EPI_BYTES + (warp - 2) * F::DEPTH * F::BLOCK) + lane;
+    float* st = reinterpret_cast<float*>(mine + (warp - FIRST) * EPI_BYTES);
+    const uint4* fetched = reinterpret_cast<uint4*>(mine + EPI_WARPS * EPI_BYTES + (warp - FIRST) * F::DEPTH * F::BLOCK) + lane;
     const DropKey key = drop_key(p.drop);
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -750,16 +782,19 @@ __global__ void __launch_bounds__(THREADS, 1)
       };
 #pragma unroll
       for (int k = 0; k < F::DEPTH; ++k) fetch(k);  // while the main loop runs
-      // warp-uniform outcome: the tcgen05.ld below is warp-collective
-      if (__any_sync(0xffffffffu, *abort_flag) ||
-          !__all_sync(0xffffffffu, wait_or_look(smem_u32(&tfull[acc]), acc_phase, limit))) {
-        record_error(p.err, DEV_TIMEOUT_EPILOGUE);
-        *abort_flag = 1;
-        break;
-      }
-      tc_fence_after();
-      const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * 256 + share;
-      // Hands the accumulator back as soon as its last columns are in registers.
+      // Waits for the next accumulator; warp-uniform outcome, for the tcgen05.ld
+      // below is warp-collective.
+      auto ready = [&] {
+        if (__any_sync(0xffffffffu, *abort_flag) ||
+            !__all_sync(0xffffffffu, wait_or_look(smem_u32(&tfull[acc]), acc_phase, limit))) {
+          record_error(p.err, DEV_TIMEOUT_EPILOGUE);
+          *abort_flag = 1;
+          return false;
+        }
+        tc_fence_after();
+        return true;
+      };
+      // Hands it back, once its last columns are in registers.
       auto release = [&] {
         tc_fence_before();
         __syncwarp();
@@ -770,39 +805,84 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_arrive(&tempty[acc]);
         }
       };
-      if (blocks <= 0) release();
-#pragma unroll 1
-      for (int k = 0; k < blocks; ++k) {
-        const int col = col0 + 32 * k + Lay<EPI>::col(lane);  // this lane's first column
-        uint32_t a[32];
-        tmem_ld_32x32b_x32(tbase + 32 * k, a);
-        if (GATED) {
-          uint32_t b[32];
-          tmem_ld_32x32b_x32(tbase + width + 32 * k, b);
-          tmem_ld_wait();
-          if (k == blocks - 1) release();
-          MT_WITH_ACT(p.act, (gated_block<ACT>(p, row0, col, end, lane, reinterpret_cast<uint4*>(st), a, b)));
-        } else {
-          tmem_ld_wait();
-          if (k == blocks - 1) release();
-          stage_f32(st, lane, a);
-          __syncwarp();
-          Aux aux;
-          if (reads_aux<EPI>(p)) {  // its slots exist only then
-            copy_wait<F::DEPTH - 1>();
-            if (inside(k))
-              fetched_aux<EPI>(fetched + k % F::DEPTH * (F::BLOCK / 16), aux);
-            else
-              load_aux<EPI>(p, row0, col, end, aux);
-          }
-          block<EPI>(p, key, inside(k), row0, col, end, lane, st, aux);
-          fetch(k + F::DEPTH);
+      auto next = [&] {
+        if (++acc == 2) {
+          acc = 0;
+          acc_phase ^= 1;
         }
+      };
+      auto columns = [&](int k) {  // of block k in tensor memory
+        return tmem_base + ((uint32_t)(quarter * 32) << 16) + acc * 256 + share + 32 * k;
+      };
+      // What becomes of block k once its sums are in registers.
+      auto finish = [&](int k, const uint32_t(&a)[32]) {
+        const int col = col0 + 32 * k + Lay<EPI>::col(lane);  // this lane's first column
+        stage_f32(st, lane, a);
+        __syncwarp();
+        Aux aux;
+        if (reads_aux<EPI>(p)) {  // its slots exist only then
+          copy_wait<F::DEPTH - 1>();
+          if (inside(k))
+            fetched_aux<EPI>(fetched + k % F::DEPTH * (F::BLOCK / 16), aux);
+          else
+            load_aux<EPI>(p, row0, col, end, aux);
+        }
+        block<EPI>(p, key, inside(k), row0, col, end, lane, st, aux);
+        fetch(k + F::DEPTH);
         __syncwarp();  // the buffer is free for the next block
-      }
-      if (++acc == 2) {
-        acc = 0;
-        acc_phase ^= 1;
+      };
+      if constexpr (CHUNKED) {
+        uint32_t sum[4][32];
+        bool ok = true;
+        for (int kb0 = 0; kb0 < num_kb; kb0 = chunk_end(kb0)) {
+          if (!(ok = ready())) break;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (k >= blocks) break;
+            if (kb0 == 0) {
+              tmem_ld_32x32b_x32(columns(k), sum[k]);
+              tmem_ld_wait();
+            } else {
+              uint32_t a[32];
+              tmem_ld_32x32b_x32(columns(k), a);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                sum[k][e] = __float_as_uint(__uint_as_float(sum[k][e]) + __uint_as_float(a[e]));
+            }
+          }
+          release();
+          next();
+        }
+        if (!ok) break;
+#pragma unroll 1
+        for (int k = 0; k < blocks; ++k) {
+          finish(k, sum[0]);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) sum[0][e] = sum[1][e], sum[1][e] = sum[2][e], sum[2][e] = sum[3][e];
+        }
+      } else {
+        if (!ready()) break;
+        if (blocks <= 0) release();
+#pragma unroll 1
+        for (int k = 0; k < blocks; ++k) {
+          uint32_t a[32];
+          tmem_ld_32x32b_x32(columns(k), a);
+          if constexpr (GATED) {
+            uint32_t b[32];
+            tmem_ld_32x32b_x32(columns(k) + width, b);
+            tmem_ld_wait();
+            if (k == blocks - 1) release();
+            const int col = col0 + 32 * k + Lay<EPI>::col(lane);
+            MT_WITH_ACT(p.act, (gated_block<ACT>(p, row0, col, end, lane, reinterpret_cast<uint4*>(st), a, b)));
+            __syncwarp();  // the buffer is free for the next block
+          } else {
+            tmem_ld_wait();
+            if (k == blocks - 1) release();
+            finish(k, a);
+          }
+        }
+        next();
       }
     }
     copy_wait<0>();  // also where the loop was left early
@@ -863,11 +943,31 @@ LastWave last_wave(int rest, int n, bool mn_major) {
   return best;
 }
 
-template <bool PAIR, int EPI, bool WIDE>
+// Chunks of n k-blocks. One of c loses 6.1e-8 c of itself, so n of them in
+// chunks c_i lose 6.1e-8 sum c_i^2 / n: at most 14.8 for 9e-7. The first two are
+// as long as that allows (up to 20), for the tensor cores have nothing but those
+// two to do while the epilogue warps finish the tile before; the rest have 12 at
+// most.
+struct Chunks {
+  int first, rest;
+};
+Chunks chunks_of(int n) {
+  for (int first = n < 20 ? n : 20; first > 12; --first) {
+    const int left = n - 2 * first > 0 ? n - 2 * first : 0, second = n - first < first ? n - first : first;
+    const int rest = left ? (left + (left + 11) / 12 - 1) / ((left + 11) / 12) : first;
+    // left k-blocks in chunks of rest, the last one shorter
+    const int full = left / rest, last = left - full * rest;
+    const int lost = first * first + second * second + full * rest * rest + last * last;
+    if (10 * lost <= 148 * n) return Chunks{first, rest};
+  }
+  return Chunks{12, 12};
+}
+
+template <bool PAIR, int EPI, bool WIDE, bool CHUNKED>
 int launch(Op o, int bn, int device, int num_sms, cudaStream_t st) {
   constexpr bool GATED = EPI == E_GATED, B_MN = EPI == E_BWD || EPI == E_GATED_BWD;
   constexpr int TILE_M = PAIR ? 2 * BM : BM;
-  auto kernel = k_linear<PAIR, EPI, WIDE>;
+  auto kernel = k_linear<PAIR, EPI, WIDE, CHUNKED>;
   Params& p = o.p;
   // Rows of A behind the last are not staged: an MMA then reads what lies
   // behind them in shared memory, and only its rows that are not stored see it.
@@ -882,6 +982,12 @@ int launch(Op o, int bn, int device, int num_sms, cudaStream_t st) {
   p.t.sub = kb_bytes > 16384 ? 1 : kb_bytes > 8192 ? 2 : 4;
   if (p.t.sub > num_kb) p.t.sub = num_kb;
   const int stage = p.t.sub * kb_bytes;
+  // Without a bias gradient the backward's outputs are bf16 and need no chunks.
+  if (CHUNKED) {  // multiples of sub, and num_kb > CHUNK_MOST
+    const Chunks c = chunks_of(num_kb);
+    p.t.chunk_first = c.first / p.t.sub * p.t.sub;
+    p.t.chunk_rest = c.rest > p.t.sub ? c.rest / p.t.sub * p.t.sub : p.t.sub;
+  }
   const int fit = (SMEM_MOST - 1024 - BAR_BYTES - epi) / stage;
   p.t.stages = fit < MAX_STAGES ? fit : MAX_STAGES;
   // An MMA on fewer staged rows of A still reads 16 KB from the stage's start.
@@ -898,7 +1004,7 @@ int launch(Op o, int bn, int device, int num_sms, cudaStream_t st) {
   if (!ok) return MT_ERR_ARG;
 
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(THREADS, 1, 1);
+  cfg.blockDim = dim3(Warps<CHUNKED>::THREADS, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -916,6 +1022,11 @@ int launch(Op o, int bn, int device, int num_sms, cudaStream_t st) {
   if (resident[device] == 0) {
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_MOST) != cudaSuccess)
       return MT_ERR_CUDA;
+    // The epilogue warps would wait for ever for registers that the block was not launched with.
+    using W = Warps<CHUNKED>;
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, kernel) != cudaSuccess) return MT_ERR_CUDA;
+    if (CHUNKED && fa.numRegs * W::THREADS < W::FEW * 32 * W::FIRST + W::MANY * 32 * EPI_WARPS) return MT_ERR_CONFIG;
     int r = PAIR ? num_sms / 2 : num_sms;
     if (PAIR) {
       int n = 0;
@@ -981,9 +1092,17 @@ int dispatch(const Op& o, cudaStream_t st) {
     for (int bn = 256; bn >= (B_MN ? 128 : 64); bn -= B_MN ? 128 : 32) consider(bn, true);
   if (family != 2)
     for (int bn = 256; bn >= (B_MN ? 64 : 32); bn -= B_MN ? 64 : 16) consider(bn, false);
-  if (best_pair && best == 256) return launch<true, EPI, true>(o, best, device, sms, st);
-  return best_pair ? launch<true, EPI, false>(o, best, device, sms, st)
-                   : launch<false, EPI, false>(o, best, device, sms, st);
+  if constexpr (may_chunk(EPI)) {
+    // Without a bias gradient the backward's outputs are bf16 and need no chunks.
+    if ((o.p.K + BK - 1) / BK > CHUNK_MOST && (EPI != E_BWD || o.p.part)) {
+      if (best_pair && best == 256) return launch<true, EPI, true, true>(o, best, device, sms, st);
+      return best_pair ? launch<true, EPI, false, true>(o, best, device, sms, st)
+                       : launch<false, EPI, false, true>(o, best, device, sms, st);
+    }
+  }
+  if (best_pair && best == 256) return launch<true, EPI, true, false>(o, best, device, sms, st);
+  return best_pair ? launch<true, EPI, false, false>(o, best, device, sms, st)
+                   : launch<false, EPI, false, false>(o, best, device, sms, st);
 }
 
 }  // namespace

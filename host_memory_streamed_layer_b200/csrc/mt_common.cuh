@@ -376,6 +376,19 @@ __device__ __forceinline__ void umma_commit_both(uint32_t bar) {
 }
 
 // ---------------------------------------------------------------------------
+// Registers of a thread from here on, for all warps of a warpgroup. Raising
+// draws on what the block was launched with, so the shares have to add up.
+// ---------------------------------------------------------------------------
+template <int N>
+__device__ __forceinline__ void lower_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void raise_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// ---------------------------------------------------------------------------
 // Small numeric helpers.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ float warp_sum(float v) {

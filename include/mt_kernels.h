@@ -180,9 +180,10 @@ int mt_k_gemm_bf16_rope(const void* A, int64_t lda, const void* B, int64_t ldb, 
  *     pitch is a multiple of 4 (fp32) or 8 (bf16) elements. Widths may be odd:
  *     nothing behind a row's last element is read or written;
  *   - all sums, statistics and activations are fp32; a bf16 output is rounded
- *     once, to nearest even, from the fp32 result. A product of depth K is
- *     accumulated by the tensor cores, which truncate: as in mt_k_gemm_bf16 it
- *     comes out low by about 1.1e-9 K of itself;
+ *     once, to nearest even, from the fp32 result. The tensor cores truncate as
+ *     they accumulate (a product of depth K comes out low by about 1e-9 K of
+ *     itself, as in mt_k_gemm_bf16); fp32 outputs of these calls, C and db, are
+ *     summed in pieces that keep that below 1e-6;
  *   - the calls are deterministic: the same inputs give the same bits;
  *   - buffers may not overlap unless a call allows it; scratch belongs to one
  *     call in flight at a time (calls that may run at once, captured graphs

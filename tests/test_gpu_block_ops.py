@@ -552,6 +552,31 @@ def test_gated_activations(act):
     within(h.np(), want, (HALF[torch.bfloat16] + 2.0 ** -22) * np.abs(want) + ea * np.abs(u) + (np.abs(block.act(g, act)) + ea) * eu)
 
 
+@pytest.mark.parametrize("fam", FAMILIES)
+@pytest.mark.parametrize("M,N,K", [(256, 256, 13824), (300, 1000, 2056), (5, 64, 5504), (2309, 1948, 968)])
+def test_fp32_outputs_keep_their_digits_at_any_depth(M, N, K, fam):
+    """Long sums in fp32 outputs: the accumulator is added up after at most 15
+    k-blocks of 64 on average, 60 steps that each truncate half a unit, 2^-24, on
+    average: 60 x 2^-24 of the sum (relative L2). All 864 steps of K = 13824 at
+    once would lose 1.6e-5."""
+    mt = _mt()
+    g = torch.Generator(device=DEV).manual_seed(K)
+    ld = (N + 7) // 8 * 8
+    A = torch.randn(M, K, generator=g, device=DEV).bfloat16()
+    W = (torch.randn(K, ld, generator=g, device=DEV) / K ** 0.5).bfloat16()
+    Wt = W[:, :N].t().contiguous()
+    C, dZ = torch.zeros(M, ld, device=DEV), torch.zeros(M, ld, dtype=torch.bfloat16, device=DEV)
+    part, db = scratch(mt.mt_k_linear_bwd_act_partial_floats(M, N)), scratch(N)
+    with family(fam):
+        mt.mt_k_linear_fwd(A.data_ptr(), K, Wt.data_ptr(), K, 0, 0, None, 0, 0, 0, 0, C.data_ptr(), 0, ld, M, N, K, stream())
+        mt.mt_k_linear_bwd_act(A.data_ptr(), K, W.data_ptr(), ld, 0, 0, 0, None, dZ.data_ptr(), ld, part.data_ptr(), db.data_ptr(),
+                               M, N, K, stream())
+    want = A.double() @ W[:, :N].double()
+    for got, ref in [(C[:, :N], want), (db[:N], want.sum(0))]:
+        assert float((got.double() - ref).norm() / ref.norm()) <= 60 * 2.0 ** -24
+    assert float((dZ[:, :N].double() - want).norm() / want.norm()) <= 2.0 ** -8
+
+
 @pytest.mark.parametrize("fam", [0, 2])
 @pytest.mark.parametrize("M,N,K", [(2309, 1948, 136), (2309, 2048, 64), (4000, 1300, 200), (19200, 264, 40)])
 def test_a_last_wave_of_narrower_tiles(M, N, K, fam):
