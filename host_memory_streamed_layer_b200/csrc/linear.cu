@@ -25,10 +25,12 @@
 // tensor cores, in which each SM fetches 32 KB (the L2 gives an SM about 60
 // bytes a cycle) and moves 64 KB through its shared memory, whose 128 bytes a
 // cycle are so nearly used up that each byte the epilogue moves there costs
-// time. Measured at 16384 x 5504 x 2048 on one B200, interleaved with
-// torch.matmul of the same product at 278 us: 270 us with a bias alone, 291 us
-// with GELU and the pre-activation kept, 300 us for the backward step with the
-// bias gradient; 8192 x 13824 x 5120 gated 1512 us (1534 TFLOP/s) beside 1638.
+// time. Measured at 16384 x 5504 x 2048 on one B200, interleaved with a library's
+// plain product at 248 us: 251 us with a bias alone, 273 us with GELU and the
+// pre-activation kept, 310 us for the backward step with the bias gradient;
+// 8192 x 13824 x 5120 gated, the halves kept, 1512 us (1534 TFLOP/s) beside 1638.
+// Back to back for long, the card's power limit holds all of them to about 1390
+// TFLOP/s.
 #include <type_traits>
 
 #include "act_dropout.cuh"
@@ -540,217 +542,217 @@ __global__ void __launch_bounds__(Warps<CHUNKED>::THREADS, 1)
   const int tile_step = PAIR ? gridDim.x >> 1 : gridDim.x;
 
   if (warp < FIRST) {
-  if (CHUNKED) lower_registers<Warps<CHUNKED>::FEW>();
-  if (warp == 0) {
-    // ---------------- TMA producer (the whole warp; one elected lane copies) ----------------
-    int stage = 0;
-    uint32_t phase = 0;
-    int issued = 0;  // stages filled so far (for the teardown)
-    const uint32_t fb0 = PAIR ? mapa_shared(smem_u32(&full[0]), 0) : 0;  // the leader's full barriers
-    const uint32_t empty0 = smem_u32(&empty[0]);
-    bool ok = true;
-    for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
-      int mb, first, width;
-      tile_at(tile, mb, first, width);
-      const int m0 = mb * TILE_M + (int)rank * BM;
-      // A pair's B rows are split over its CTAs; a gated tile has one half from each weight.
-      const int n0 = first + (PAIR && !GATED ? (int)rank * (width / 2) : 0);
-      const bool cut = WIDE && width < on;  // tmS, tmS2: the same weights by fewer rows
-      const CUtensorMap* mB = PAIR && GATED && rank ? (cut ? &tmS2 : &tmB2) : cut ? &tmS : &tmB;
-      const int rows = cut ? b_rows / split : b_rows;
-      const uint32_t bytes = a_bytes + rows * (BK * 2);
-      for (int kb = 0; kb < num_kb; kb += sub) {
-        const bool got = wait_or_look(empty0 + 8 * stage, phase ^ 1, limit);
-        if (!__all_sync(0xffffffffu, got && !*abort_flag)) {
-          ok = false;
-          break;
-        }
-        uint8_t* sa = smem + stage * stage_bytes;
-        const int n = min(sub, num_kb - kb);  // k-blocks of this stage
-        int k0 = kb * BK;
-        if (elect_one()) {
-          const uint32_t fb = fb0 + 8 * stage;
-          if (!PAIR || rank == 0) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * n * bytes);
-          auto load = [&] {
-            uint8_t* sb = sa + a_bytes;
-            if (PAIR) {
-              tma_load_2d_pair(sa, &tmA, fb, k0, m0);
-              if (!B_MN) {
-                tma_load_2d_pair(sb, mB, fb, k0, n0);
-              } else {
-                tma_load_2d_pair(sb, mB, fb, n0, k0);
-                if (rows > 64) tma_load_2d_pair(sb + 8192, mB, fb, n0 + 64, k0);
-              }
-            } else {
-              tma_load_2d(sa, &tmA, &full[stage], k0, m0);
-              if (GATED) {
-                tma_load_2d(sb, &tmB, &full[stage], k0, n0);
-                tma_load_2d(sb + (kb_bytes - a_bytes) / 2, &tmB2, &full[stage], k0, n0);
-              } else if (!B_MN) {
-                tma_load_2d(sb, &tmB, &full[stage], k0, n0);
-              } else {
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                  if (c * 64 < b_rows) tma_load_2d(sb + c * 8192, &tmB, &full[stage], n0 + c * 64, k0);
-              }
-            }
-          };
-          load();
-#pragma unroll 1
-          for (int i = 1; i < n; ++i) {
-            sa += kb_bytes, k0 += BK;
-            load();
-          }
-        }
-        ++issued;
-        if (++stage == stages) {
-          stage = 0;
-          phase ^= 1;
-        }
-      }
-    }
-    if (!ok && lane == 0) {
-      record_error(p.err, DEV_TIMEOUT_PRODUCER);
-      *abort_flag = 1;
-    }
-    __syncwarp();
-    if (lane == 0) {
-      if (ok) {
-        // Wait until the MMA has released every stage, so that no commit is on
-        // its way to this CTA's barriers when it exits. If another role gives
-        // up meanwhile, the MMA may never release them: drain the copies below.
-        for (int i = 0; i < stages && ok; ++i) {
-          const uint64_t t0 = globaltimer();
-          while (!mbar_wait(&empty[stage], phase ^ 1, 0)) {
-            if (!PAIR && *abort_flag) {
-              ok = false;
-              break;
-            }
-            if (globaltimer() - t0 > kWaitLimitNs) {
-              record_error(p.err, DEV_TIMEOUT_TEARDOWN);
-              *abort_flag = 1;
-              ok = false;
-              break;
-            }
-          }
-          if (++stage == stages) {
-            stage = 0;
-            phase ^= 1;
-          }
-        }
-      }
-      if (!ok && rank == 0) {
-        // Every issued copy lands before the shared memory goes away: stage s
-        // was last filled by fill s + STAGES q (the largest below `issued`), in
-        // phase q mod 2. The leader's barriers count both CTAs' bytes.
-        for (int s = 0; s < stages && s < issued; ++s) {
-          const int q = (issued - 1 - s) / stages;
-          if (!mbar_wait(&full[s], (uint32_t)(q & 1))) record_error(p.err, DEV_TIMEOUT_TEARDOWN);
-        }
-      }
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    if (rank == 0) {
-      // ---------------- MMA issuer ----------------
-      // The whole warp walks the loop and one elected lane issues: with the
-      // loop inside one lane's branch, every MMA and commit first moved its
-      // operands to uniform registers, and a k-block took 560 cycles and more
-      // to issue where the tensor core needs 512.
-      const uint32_t idesc_whole = idesc_bf16_f32(TILE_M, bn, false, B_MN);
-      const uint32_t idesc_cut = idesc_bf16_f32(TILE_M, bn / split, false, B_MN);
-      // Descriptors of stage 0; stages and k-steps only move the start address.
-      const uint32_t s0 = smem_u32(smem);
-      const uint64_t a0 = sdesc_sw128(s0, 16, 1024);
-      const uint64_t b0 = sdesc_sw128(s0 + a_bytes, B_MN ? 8192 : 16, 1024);
-      const uint32_t kStage = stage_bytes >> 4, kBlock = kb_bytes >> 4;
-      constexpr uint32_t kAStep = 32 >> 4, kBStep = (B_MN ? 2048 : 32) >> 4;
-      const uint32_t full0 = smem_u32(&full[0]), empty0 = smem_u32(&empty[0]), tfull0 = smem_u32(&tfull[0]);
+    if (CHUNKED) lower_registers<Warps<CHUNKED>::FEW>();
+    if (warp == 0) {
+      // ---------------- TMA producer (the whole warp; one elected lane copies) ----------------
       int stage = 0;
       uint32_t phase = 0;
-      int acc = 0;
-      uint32_t acc_phase = 0;
+      int issued = 0;  // stages filled so far (for the teardown)
+      const uint32_t fb0 = PAIR ? mapa_shared(smem_u32(&full[0]), 0) : 0;  // the leader's full barriers
+      const uint32_t empty0 = smem_u32(&empty[0]);
       bool ok = true;
-      bool issued = false;
-      for (int tile = first_tile, kb0 = 0; tile < num_tiles && ok;) {
-        const bool free_acc = PAIR ? mbar_wait_cluster(&tempty[acc], acc_phase ^ 1)
-                                   : wait_or_look(smem_u32(&tempty[acc]), acc_phase ^ 1, limit);
-        if (!__all_sync(0xffffffffu, free_acc && !*abort_flag)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + acc * 256;
-        const uint32_t idesc = WIDE && tile >= whole ? idesc_cut : idesc_whole;
-        const int kb1 = chunk_end(kb0);
-        for (int kb = kb0; kb < kb1; kb += sub) {
-          if (!__all_sync(0xffffffffu, wait_or_look(full0 + 8 * stage, phase, limit))) {
+      for (int tile = first_tile; tile < num_tiles && ok; tile += tile_step) {
+        int mb, first, width;
+        tile_at(tile, mb, first, width);
+        const int m0 = mb * TILE_M + (int)rank * BM;
+        // A pair's B rows are split over its CTAs; a gated tile has one half from each weight.
+        const int n0 = first + (PAIR && !GATED ? (int)rank * (width / 2) : 0);
+        const bool cut = WIDE && width < on;  // tmS, tmS2: the same weights by fewer rows
+        const CUtensorMap* mB = PAIR && GATED && rank ? (cut ? &tmS2 : &tmB2) : cut ? &tmS : &tmB;
+        const int rows = cut ? b_rows / split : b_rows;
+        const uint32_t bytes = a_bytes + rows * (BK * 2);
+        for (int kb = 0; kb < num_kb; kb += sub) {
+          const bool got = wait_or_look(empty0 + 8 * stage, phase ^ 1, limit);
+          if (!__all_sync(0xffffffffu, got && !*abort_flag)) {
             ok = false;
             break;
           }
-          // The stage's bytes were written by TMA and published through this
-          // mbarrier, which orders them for the MMAs' reads: no tcgen05 fence.
-          uint64_t ad = a0 + stage * kStage, bd = b0 + stage * kStage;
-          const int n = min(sub, kb1 - kb);
+          uint8_t* sa = smem + stage * stage_bytes;
+          const int n = min(sub, num_kb - kb);  // k-blocks of this stage
+          int k0 = kb * BK;
           if (elect_one()) {
-            auto multiply = [&](bool accumulate) {
+            const uint32_t fb = fb0 + 8 * stage;
+            if (!PAIR || rank == 0) mbar_arrive_expect_tx(&full[stage], (PAIR ? 2 : 1) * n * bytes);
+            auto load = [&] {
+              uint8_t* sb = sa + a_bytes;
+              if (PAIR) {
+                tma_load_2d_pair(sa, &tmA, fb, k0, m0);
+                if (!B_MN) {
+                  tma_load_2d_pair(sb, mB, fb, k0, n0);
+                } else {
+                  tma_load_2d_pair(sb, mB, fb, n0, k0);
+                  if (rows > 64) tma_load_2d_pair(sb + 8192, mB, fb, n0 + 64, k0);
+                }
+              } else {
+                tma_load_2d(sa, &tmA, &full[stage], k0, m0);
+                if (GATED) {
+                  tma_load_2d(sb, &tmB, &full[stage], k0, n0);
+                  tma_load_2d(sb + (kb_bytes - a_bytes) / 2, &tmB2, &full[stage], k0, n0);
+                } else if (!B_MN) {
+                  tma_load_2d(sb, &tmB, &full[stage], k0, n0);
+                } else {
 #pragma unroll
-              for (int kk = 0; kk < BK / 16; ++kk) {
-                if (PAIR)
-                  umma_bf16_pair(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, accumulate || kk != 0);
-                else
-                  umma_bf16(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, accumulate || kk != 0);
+                  for (int c = 0; c < 4; ++c)
+                    if (c * 64 < b_rows) tma_load_2d(sb + c * 8192, &tmB, &full[stage], n0 + c * 64, k0);
+                }
               }
             };
-            multiply(kb != kb0);
+            load();
 #pragma unroll 1
             for (int i = 1; i < n; ++i) {
-              ad += kBlock, bd += kBlock;
-              multiply(true);
-            }
-            if (PAIR)
-              umma_commit_both(empty0 + 8 * stage);
-            else
-              umma_commit_u32(empty0 + 8 * stage);
-            if (kb + n == kb1) {
-              if (PAIR)
-                umma_commit_both(tfull0 + 8 * acc);
-              else
-                umma_commit_u32(tfull0 + 8 * acc);
+              sa += kb_bytes, k0 += BK;
+              load();
             }
           }
-          issued = true;
+          ++issued;
           if (++stage == stages) {
             stage = 0;
             phase ^= 1;
           }
         }
-        if (!ok) break;
-        if (++acc == 2) {
-          acc = 0;
-          acc_phase ^= 1;
-        }
-        kb0 = kb1;
-        if (kb1 == num_kb) kb0 = 0, tile += tile_step;
       }
       if (!ok && lane == 0) {
-        record_error(p.err, DEV_TIMEOUT_MMA);
+        record_error(p.err, DEV_TIMEOUT_PRODUCER);
         *abort_flag = 1;
       }
-      // Every MMA issued here completes before tensor memory is freed, also
-      // when the epilogue gave up on an accumulator it will never read.
-      if (issued) {
-        if (elect_one()) {
-          if (PAIR)
-            umma_commit_pair(smem_u32(drain));
-          else
-            umma_commit(drain);
+      __syncwarp();
+      if (lane == 0) {
+        if (ok) {
+          // Wait until the MMA has released every stage, so that no commit is on
+          // its way to this CTA's barriers when it exits. If another role gives
+          // up meanwhile, the MMA may never release them: drain the copies below.
+          for (int i = 0; i < stages && ok; ++i) {
+            const uint64_t t0 = globaltimer();
+            while (!mbar_wait(&empty[stage], phase ^ 1, 0)) {
+              if (!PAIR && *abort_flag) {
+                ok = false;
+                break;
+              }
+              if (globaltimer() - t0 > kWaitLimitNs) {
+                record_error(p.err, DEV_TIMEOUT_TEARDOWN);
+                *abort_flag = 1;
+                ok = false;
+                break;
+              }
+            }
+            if (++stage == stages) {
+              stage = 0;
+              phase ^= 1;
+            }
+          }
         }
-        __syncwarp();
-        if (!mbar_wait(drain, 0) && lane == 0) record_error(p.err, DEV_TIMEOUT_TEARDOWN);
+        if (!ok && rank == 0) {
+          // Every issued copy lands before the shared memory goes away: stage s
+          // was last filled by fill s + STAGES q (the largest below `issued`), in
+          // phase q mod 2. The leader's barriers count both CTAs' bytes.
+          for (int s = 0; s < stages && s < issued; ++s) {
+            const int q = (issued - 1 - s) / stages;
+            if (!mbar_wait(&full[s], (uint32_t)(q & 1))) record_error(p.err, DEV_TIMEOUT_TEARDOWN);
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      if (rank == 0) {
+        // ---------------- MMA issuer ----------------
+        // The whole warp walks the loop and one elected lane issues: with the
+        // loop inside one lane's branch, every MMA and commit first moved its
+        // operands to uniform registers, and a k-block took 560 cycles and more
+        // to issue where the tensor core needs 512.
+        const uint32_t idesc_whole = idesc_bf16_f32(TILE_M, bn, false, B_MN);
+        const uint32_t idesc_cut = idesc_bf16_f32(TILE_M, bn / split, false, B_MN);
+        // Descriptors of stage 0; stages and k-steps only move the start address.
+        const uint32_t s0 = smem_u32(smem);
+        const uint64_t a0 = sdesc_sw128(s0, 16, 1024);
+        const uint64_t b0 = sdesc_sw128(s0 + a_bytes, B_MN ? 8192 : 16, 1024);
+        const uint32_t kStage = stage_bytes >> 4, kBlock = kb_bytes >> 4;
+        constexpr uint32_t kAStep = 32 >> 4, kBStep = (B_MN ? 2048 : 32) >> 4;
+        const uint32_t full0 = smem_u32(&full[0]), empty0 = smem_u32(&empty[0]), tfull0 = smem_u32(&tfull[0]);
+        int stage = 0;
+        uint32_t phase = 0;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        bool ok = true;
+        bool issued = false;
+        for (int tile = first_tile, kb0 = 0; tile < num_tiles && ok;) {
+          const bool free_acc = PAIR ? mbar_wait_cluster(&tempty[acc], acc_phase ^ 1)
+                                     : wait_or_look(smem_u32(&tempty[acc]), acc_phase ^ 1, limit);
+          if (!__all_sync(0xffffffffu, free_acc && !*abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d_tmem = tmem_base + acc * 256;
+          const uint32_t idesc = WIDE && tile >= whole ? idesc_cut : idesc_whole;
+          const int kb1 = chunk_end(kb0);
+          for (int kb = kb0; kb < kb1; kb += sub) {
+            if (!__all_sync(0xffffffffu, wait_or_look(full0 + 8 * stage, phase, limit))) {
+              ok = false;
+              break;
+            }
+            // The stage's bytes were written by TMA and published through this
+            // mbarrier, which orders them for the MMAs' reads: no tcgen05 fence.
+            uint64_t ad = a0 + stage * kStage, bd = b0 + stage * kStage;
+            const int n = min(sub, kb1 - kb);
+            if (elect_one()) {
+              auto multiply = [&](bool accumulate) {
+#pragma unroll
+                for (int kk = 0; kk < BK / 16; ++kk) {
+                  if (PAIR)
+                    umma_bf16_pair(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, accumulate || kk != 0);
+                  else
+                    umma_bf16(d_tmem, ad + kk * kAStep, bd + kk * kBStep, idesc, accumulate || kk != 0);
+                }
+              };
+              multiply(kb != kb0);
+#pragma unroll 1
+              for (int i = 1; i < n; ++i) {
+                ad += kBlock, bd += kBlock;
+                multiply(true);
+              }
+              if (PAIR)
+                umma_commit_both(empty0 + 8 * stage);
+              else
+                umma_commit_u32(empty0 + 8 * stage);
+              if (kb + n == kb1) {
+                if (PAIR)
+                  umma_commit_both(tfull0 + 8 * acc);
+                else
+                  umma_commit_u32(tfull0 + 8 * acc);
+              }
+            }
+            issued = true;
+            if (++stage == stages) {
+              stage = 0;
+              phase ^= 1;
+            }
+          }
+          if (!ok) break;
+          if (++acc == 2) {
+            acc = 0;
+            acc_phase ^= 1;
+          }
+          kb0 = kb1;
+          if (kb1 == num_kb) kb0 = 0, tile += tile_step;
+        }
+        if (!ok && lane == 0) {
+          record_error(p.err, DEV_TIMEOUT_MMA);
+          *abort_flag = 1;
+        }
+        // Every MMA issued here completes before tensor memory is freed, also
+        // when the epilogue gave up on an accumulator it will never read.
+        if (issued) {
+          if (elect_one()) {
+            if (PAIR)
+              umma_commit_pair(smem_u32(drain));
+            else
+              umma_commit(drain);
+          }
+          __syncwarp();
+          if (!mbar_wait(drain, 0) && lane == 0) record_error(p.err, DEV_TIMEOUT_TEARDOWN);
+        }
       }
     }
-  }
   } else {
     if (CHUNKED) raise_registers<Warps<CHUNKED>::MANY>();
     // ---------------- epilogue ----------------
