@@ -30,7 +30,8 @@ template <int W>
 constexpr int ROWS = 8 / W;
 
 template <int W>
-__device__ __forceinline__ void drop_piece(float (&v)[W], int col, uint32_t row, const DropDesc& drop, const DropKey& key) {
+__device__ __forceinline__ void drop_piece(float (&v)[W], int col, uint32_t row, const DropDesc& drop,
+                                           const DropKey& key) {
 #pragma unroll
   for (int h = 0; h < W / 4; ++h) drop4(v + 4 * h, (col >> 2) + h, row, drop, key);
 }
@@ -219,7 +220,8 @@ int launch_dropout(const void* x, int x_type, int64_t ldx, const DropDesc& drop,
 }
 
 size_t act_bwd_partial_floats(int M, int N) {
-  const int a = grid_for(M, N, 4, kActBwdBlocks).gy, b = grid_for(M, N, 8, kActBwdBlocks).gy;  // dc's type is not known here
+  // dc's type is not known here
+  const int a = grid_for(M, N, 4, kActBwdBlocks).gy, b = grid_for(M, N, 8, kActBwdBlocks).gy;
   return (size_t)(a > b ? a : b) * N;
 }
 

@@ -174,7 +174,8 @@ __global__ void __launch_bounds__(LnBwd<X, Y, TX, G>::THREADS, LnBwd<X, Y, TX, G
   const int64_t r1 = min((int64_t)T, r0 + rows_per_block);
   const int groups = r1 > r0 ? (int)((r1 - r0 + RY - 1) / RY) : 0;
   // This lane's slots of a stage: G pieces of x, of dres, of dy.
-  const uint32_t mine = smem_u32(ring) + threadIdx.x * L::PX, mine_y = smem_u32(ring) + L::THREADS * G * 2 * L::PX + threadIdx.x * L::PY;
+  const uint32_t mine = smem_u32(ring) + threadIdx.x * L::PX;
+  const uint32_t mine_y = smem_u32(ring) + L::THREADS * G * 2 * L::PX + threadIdx.x * L::PY;
   auto fetch = [&](int i) {  // row group i, one group of copies (empty behind the last)
     const int64_t row = r0 + (int64_t)i * RY + ty;
     if (EXACT && i < groups && row < r1) {
@@ -210,8 +211,9 @@ __global__ void __launch_bounds__(LnBwd<X, Y, TX, G>::THREADS, LnBwd<X, Y, TX, G
     for (int k = 0; k < G; ++k) {
       const int c = (tx + k * TX) * W, n = ok ? d - c : 0;
       if (EXACT) {
-        const uint8_t* at = ring + i % S * L::ROWS_BYTES + threadIdx.x * L::PX + k * L::THREADS * L::PX;
-        const uint8_t* at_y = ring + i % S * L::ROWS_BYTES + L::THREADS * (G * 2 * L::PX + k * L::PY) + threadIdx.x * L::PY;
+        const uint8_t* stage = ring + i % S * L::ROWS_BYTES;
+        const uint8_t* at = stage + k * L::THREADS * L::PX + threadIdx.x * L::PX;
+        const uint8_t* at_y = stage + L::THREADS * (G * 2 * L::PX + k * L::PY) + threadIdx.x * L::PY;
         load_piece<W, true>(reinterpret_cast<const X*>(at), n, xv[k]);
         load_piece<W, true>(reinterpret_cast<const Y*>(at_y), n, dv[k]);
         if (dres) load_piece<W, true>(reinterpret_cast<const X*>(at + G * L::THREADS * L::PX), n, rv[k]);
@@ -400,7 +402,8 @@ int launch_column_sums(const float* part, int rows, int64_t pitch, int n, float*
 int launch_layernorm_fwd(const void* x, int x_type, int64_t ldx, const void* g, const void* b, void* y, int y_type,
                          int64_t ldy, float* mean, float* rstd, int T, int d, float eps, cudaStream_t st) {
   if (T <= 0) return MT_OK;
-  if (x_type == MT_F32 && y_type == MT_F32) return ln_fwd<float, float>(x, ldx, g, b, y, ldy, mean, rstd, T, d, eps, st);
+  if (x_type == MT_F32 && y_type == MT_F32)
+    return ln_fwd<float, float>(x, ldx, g, b, y, ldy, mean, rstd, T, d, eps, st);
   if (x_type == MT_F32) return ln_fwd<float, bf16>(x, ldx, g, b, y, ldy, mean, rstd, T, d, eps, st);
   if (y_type == MT_F32) return ln_fwd<bf16, float>(x, ldx, g, b, y, ldy, mean, rstd, T, d, eps, st);
   return ln_fwd<bf16, bf16>(x, ldx, g, b, y, ldy, mean, rstd, T, d, eps, st);

@@ -386,20 +386,13 @@ __device__ __forceinline__ void gated_bwd_block(const Params& p, int row0, int c
 }
 
 // One block with its activation and fullness as constants.
-template <int EPI>
-__device__ __forceinline__ void block(const Params& p, const DropKey& key, bool full, int row0, int col, int end,
-                                      int lane, const float* st, const Aux& a) {
-  if (full) {
-    if (EPI == E_LINEAR_BF16) MT_WITH_ACT(p.act, (linear_block<E_LINEAR_BF16, ACT, true>(p, key, row0, col, end, lane, st, a)));
-    if (EPI == E_LINEAR_F32) MT_WITH_ACT(p.act, (linear_block<E_LINEAR_F32, ACT, true>(p, key, row0, col, end, lane, st, a)));
-    if (EPI == E_BWD) MT_WITH_ACT(p.act, (bwd_block<ACT, true>(p, key, row0, col, end, lane, st, a)));
-    if (EPI == E_GATED_BWD) MT_WITH_ACT(p.act, (gated_bwd_block<ACT, true>(p, row0, col, end, lane, st, a)));
-  } else {
-    if (EPI == E_LINEAR_BF16) MT_WITH_ACT(p.act, (linear_block<E_LINEAR_BF16, ACT, false>(p, key, row0, col, end, lane, st, a)));
-    if (EPI == E_LINEAR_F32) MT_WITH_ACT(p.act, (linear_block<E_LINEAR_F32, ACT, false>(p, key, row0, col, end, lane, st, a)));
-    if (EPI == E_BWD) MT_WITH_ACT(p.act, (bwd_block<ACT, false>(p, key, row0, col, end, lane, st, a)));
-    if (EPI == E_GATED_BWD) MT_WITH_ACT(p.act, (gated_bwd_block<ACT, false>(p, row0, col, end, lane, st, a)));
-  }
+template <int EPI, bool FULL>
+__device__ __forceinline__ void block(const Params& p, const DropKey& key, int row0, int col, int end, int lane,
+                                      const float* st, const Aux& a) {
+  if constexpr (EPI == E_LINEAR_BF16 || EPI == E_LINEAR_F32)
+    MT_WITH_ACT(p.act, (linear_block<EPI, ACT, FULL>(p, key, row0, col, end, lane, st, a)));
+  if constexpr (EPI == E_BWD) MT_WITH_ACT(p.act, (bwd_block<ACT, FULL>(p, key, row0, col, end, lane, st, a)));
+  if constexpr (EPI == E_GATED_BWD) MT_WITH_ACT(p.act, (gated_bwd_block<ACT, FULL>(p, row0, col, end, lane, st, a)));
 }
 
 // Gate and up meet in the registers of a row's lane; their bf16 blocks and h's
@@ -760,7 +753,8 @@ __global__ void __launch_bounds__(Warps<CHUNKED>::THREADS, 1)
     const int half = (warp - FIRST) >> 2;            // takes the first or the second half of the tile's blocks
     uint8_t* mine = smem + stages * stage_bytes + BAR_BYTES;
     float* st = reinterpret_cast<float*>(mine + (warp - FIRST) * EPI_BYTES);
-    const uint4* fetched = reinterpret_cast<uint4*>(mine + EPI_WARPS * EPI_BYTES + (warp - FIRST) * F::DEPTH * F::BLOCK) + lane;
+    uint8_t* ahead = mine + EPI_WARPS * EPI_BYTES + (warp - FIRST) * F::DEPTH * F::BLOCK;
+    const uint4* fetched = reinterpret_cast<uint4*>(ahead) + lane;
     const DropKey key = drop_key(p.drop);
     int acc = 0;
     uint32_t acc_phase = 0;
@@ -829,7 +823,10 @@ __global__ void __launch_bounds__(Warps<CHUNKED>::THREADS, 1)
           else
             load_aux<EPI>(p, row0, col, end, aux);
         }
-        block<EPI>(p, key, inside(k), row0, col, end, lane, st, aux);
+        if (inside(k))
+          block<EPI, true>(p, key, row0, col, end, lane, st, aux);
+        else
+          block<EPI, false>(p, key, row0, col, end, lane, st, aux);
         fetch(k + F::DEPTH);
         __syncwarp();  // the buffer is free for the next block
       };
