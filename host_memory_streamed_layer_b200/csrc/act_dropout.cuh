@@ -231,7 +231,7 @@ inline int make_drop(const mt_dropout* u, int64_t rows, DropDesc* out) {
   *out = DropDesc{0, 0, 1.f, 0, 0, nullptr, {}, {}};
   if (!u) return MT_OK;
   if (!(u->p >= 0.f) || !(u->p < 1.f)) return MT_ERR_ARG;
-  if (u->row0 < 0 || u->row0 + rows > (int64_t(1) << 32)) return MT_ERR_ARG;
+  if (u->row0 < 0 || u->row0 > (int64_t(1) << 32) - rows) return MT_ERR_ARG;  // rows <= 2^30: nothing overflows
   if (u->p == 0.f) return MT_OK;
   out->on = 1;
   out->threshold = (uint32_t)llrint((double)u->p * 4294967296.0);

@@ -1,0 +1,23 @@
+"""Limits of the layer-norm, dropout, linear and gated feed-forward calls that
+the header states, each at the border: what lies behind it is refused on the
+host, before any device work (no GPU here)."""
+import pytest
+
+from test_block_ops_refusals import _mt, refused
+
+I64_MAX = (1 << 63) - 1
+
+
+@pytest.mark.parametrize("row0", [I64_MAX, I64_MAX - 7, I64_MAX - 8, 1 << 62, (1 << 32) - 7])
+@pytest.mark.parametrize("name", ["mt_k_dropout", "mt_k_linear_fwd", "mt_k_linear_bwd_act", "mt_k_act_bwd"])
+def test_rows_of_the_mask_behind_its_counter_are_refused(name, row0):
+    """row0 + 8 rows must stay within 2^32, also where the sum passes 2^63."""
+    refused(name, drop=_mt().mt_dropout(0.1, 1, 2, 0, row0))
+
+
+def test_the_last_rows_of_the_mask_are_accepted():
+    """An empty matrix of 8 rows: the arguments are checked, nothing is launched."""
+    mt = _mt()
+    mt.mt_k_dropout(0, 0, 0, mt.mt_dropout(0.1, 1, 2, 0, (1 << 32) - 8), 0, 0, 0, 0, 0, 8, 0)
+    with pytest.raises(mt.MTError):
+        mt.mt_k_dropout(0, 0, 0, mt.mt_dropout(0.1, 1, 2, 0, I64_MAX - 3), 0, 0, 0, 0, 0, 8, 0)
