@@ -182,6 +182,11 @@ bool mat_ok(const void* p, int type, int64_t ld, int64_t width) {
   return p && al16(p) && ld >= width && ld % (type == MT_F32 ? 4 : 8) == 0;
 }
 bool opt_mat_ok(const void* p, int type, int64_t ld, int64_t width) { return !p || mat_ok(p, type, ld, width); }
+// Vectors of fp32 and dev_err (each may be NULL here) are read and written by the element.
+template <typename... P>
+bool al4(const P*... p) {
+  return ((reinterpret_cast<uintptr_t>(p) | ...) & 3) == 0;
+}
 
 // The launchers' dropout; rows: of the call. offset_dev is read as 8 bytes.
 int drop_of(const mt_dropout* d, int rows, mt::DropDesc* out) {
@@ -197,7 +202,9 @@ extern "C" int mt_k_layernorm_fwd(const void* x, int x_type, int64_t ldx, const 
   if (!type_ok(x_type) || !type_ok(y_type) || !size_ok(T) || d <= 0 || !(eps >= 0.f)) return MT_ERR_ARG;
   if (d > 8192) return MT_ERR_CONFIG;
   if (T == 0) return MT_OK;
-  if (!mat_ok(x, x_type, ldx, d) || !mat_ok(y, y_type, ldy, d) || !g || !al16(g) || !al16(b)) return MT_ERR_ARG;
+  if (!mat_ok(x, x_type, ldx, d) || !mat_ok(y, y_type, ldy, d) || !g || !al16(g) || !al16(b) ||
+      !al4(mean, rstd))
+    return MT_ERR_ARG;
   return mt::launch_layernorm_fwd(x, x_type, ldx, g, b, y, y_type, ldy, mean, rstd, T, d, eps, S(stream));
 }
 
@@ -213,7 +220,7 @@ extern "C" int mt_k_layernorm_bwd(const void* x, int x_type, int64_t ldx, const 
   if (d > 8192) return MT_ERR_CONFIG;
   if (T > 0) {
     if (!mat_ok(x, x_type, ldx, d) || !mat_ok(dy, dy_type, lddy, d) || !opt_mat_ok(dres, x_type, lddres, d) ||
-        !mat_ok(dx, x_type, lddx, d) || !g || !al16(g) || !mean || !rstd || !part)
+        !mat_ok(dx, x_type, lddx, d) || !g || !al16(g) || !mean || !rstd || !part || !al4(mean, rstd, part, dg, db))
       return MT_ERR_ARG;
     if (dx_bf16 && (x_type != MT_F32 || !mat_ok(dx_bf16, MT_BF16, lddx, d))) return MT_ERR_ARG;
   }
@@ -240,7 +247,8 @@ extern "C" int mt_k_linear_fwd(const void* A, int64_t lda, const void* W, int64_
   if (const int rc = drop_of(drop, M, &dd)) return rc;
   if (M == 0 || N == 0) return MT_OK;
   if (K == 0 || !mat_ok(A, MT_BF16, lda, K) || !mat_ok(W, MT_BF16, ldw, K) || !al16(bias) ||
-      !opt_mat_ok(R, out_type, ldr, N) || !opt_mat_ok(Z, MT_BF16, ldz, N) || !mat_ok(C, out_type, ldc, N))
+      !opt_mat_ok(R, out_type, ldr, N) || !opt_mat_ok(Z, MT_BF16, ldz, N) || !mat_ok(C, out_type, ldc, N) ||
+      !al4(dev_err))
     return MT_ERR_ARG;
   const mt::LinearFwd a{A, lda, W, ldw, bias, act, R, ldr, Z, ldz, C, out_type, ldc, M, N, K};
   return mt::launch_linear_fwd(a, dd, S(stream), dev_err);
@@ -259,7 +267,8 @@ extern "C" int mt_k_linear_bwd_act(const void* dY, int64_t lddy, const void* W, 
   if (N == 0) return MT_OK;
   if (M == 0) return !db || cudaMemsetAsync(db, 0, sizeof(float) * N, S(stream)) == cudaSuccess ? MT_OK : MT_ERR_CUDA;
   if (K == 0 || !mat_ok(dY, MT_BF16, lddy, K) || !mat_ok(W, MT_BF16, ldw, N) || !opt_mat_ok(Z, MT_BF16, ldz, N) ||
-      !mat_ok(dZ, MT_BF16, lddz, N) || (act != MT_ACT_NONE && !Z) || (db && !part) || !al16(part))
+      !mat_ok(dZ, MT_BF16, lddz, N) || (act != MT_ACT_NONE && !Z) || (db && !part) || !al16(part) ||
+      !al4(db, dev_err))
     return MT_ERR_ARG;
   const mt::LinearBwd a{dY, lddy, W, ldw, Z, ldz, act, dZ, lddz, part, db, M, N, K};
   return mt::launch_linear_bwd_act(a, dd, S(stream), dev_err);
@@ -277,7 +286,7 @@ extern "C" int mt_k_act_bwd(const void* dC, int dc_type, int64_t lddc, const voi
   if (const int rc = drop_of(drop, M, &dd)) return rc;
   if (M > 0 && N > 0 &&
       (!mat_ok(dC, dc_type, lddc, N) || !opt_mat_ok(Z, MT_BF16, ldz, N) || !mat_ok(dZ, MT_BF16, lddz, N) ||
-       (act != MT_ACT_NONE && !Z) || (db && !part)))
+       (act != MT_ACT_NONE && !Z) || (db && !part) || !al4(part, db)))
     return MT_ERR_ARG;
   return mt::launch_act_bwd(dC, dc_type, lddc, Z, ldz, act, dd, dZ, lddz, part, db, M, N, S(stream));
 }
@@ -288,7 +297,7 @@ extern "C" int mt_k_gated_ffn_fwd(const void* x, int64_t ldx, const void* Wgu, i
   if (!act_ok(act) || !size_ok(M) || !size_ok(F) || !size_ok(K) || (F % 8)) return MT_ERR_ARG;
   if (M == 0 || F == 0) return MT_OK;
   if (K == 0 || !mat_ok(x, MT_BF16, ldx, K) || !mat_ok(Wgu, MT_BF16, ldw, K) ||
-      !opt_mat_ok(gu, MT_BF16, ldgu, 2 * (int64_t)F) || !mat_ok(h, MT_BF16, ldh, F))
+      !opt_mat_ok(gu, MT_BF16, ldgu, 2 * (int64_t)F) || !mat_ok(h, MT_BF16, ldh, F) || !al4(dev_err))
     return MT_ERR_ARG;
   return mt::launch_gated_ffn_fwd(x, ldx, Wgu, ldw, act, gu, ldgu, h, ldh, M, F, K, S(stream), dev_err);
 }
@@ -300,7 +309,7 @@ extern "C" int mt_k_gated_ffn_bwd(const void* dy, int64_t lddy, const void* Wd, 
   if (M == 0 || F == 0) return MT_OK;
   if (K == 0 || !mat_ok(dy, MT_BF16, lddy, K) || !mat_ok(Wd, MT_BF16, ldw, F) ||
       !mat_ok(gu, MT_BF16, ldgu, 2 * (int64_t)F) || !mat_ok(dgu, MT_BF16, lddgu, 2 * (int64_t)F) ||
-      !opt_mat_ok(h, MT_BF16, ldh, F))
+      !opt_mat_ok(h, MT_BF16, ldh, F) || !al4(dev_err))
     return MT_ERR_ARG;
   return mt::launch_gated_ffn_bwd(dy, lddy, Wd, ldw, gu, ldgu, act, dgu, lddgu, h, ldh, M, F, K, S(stream), dev_err);
 }

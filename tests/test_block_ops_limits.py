@@ -3,7 +3,7 @@ the header states, each at the border: what lies behind it is refused on the
 host, before any device work (no GPU here)."""
 import pytest
 
-from test_block_ops_refusals import _mt, refused
+from test_block_ops_refusals import P, _mt, refused
 
 I64_MAX = (1 << 63) - 1
 
@@ -21,3 +21,19 @@ def test_the_last_rows_of_the_mask_are_accepted():
     mt.mt_k_dropout(0, 0, 0, mt.mt_dropout(0.1, 1, 2, 0, (1 << 32) - 8), 0, 0, 0, 0, 0, 8, 0)
     with pytest.raises(mt.MTError):
         mt.mt_k_dropout(0, 0, 0, mt.mt_dropout(0.1, 1, 2, 0, I64_MAX - 3), 0, 0, 0, 0, 0, 8, 0)
+
+
+@pytest.mark.parametrize("name,vectors", [
+    ("mt_k_layernorm_fwd", ("mean", "rstd")),
+    ("mt_k_layernorm_bwd", ("mean", "rstd", "part", "dg", "db")),
+    ("mt_k_linear_fwd", ("dev_err",)),
+    ("mt_k_linear_bwd_act", ("part", "db", "dev_err")),
+    ("mt_k_act_bwd", ("part", "db")),
+    ("mt_k_gated_ffn_fwd", ("dev_err",)),
+    ("mt_k_gated_ffn_bwd", ("dev_err",)),
+])
+def test_vectors_off_their_elements_boundary_are_refused(name, vectors):
+    """fp32 vectors and dev_err between two multiples of 4 bytes, which a kernel could not read or write."""
+    for v in vectors:
+        for off in (1, 2):
+            refused(name, **{v: P() + off})
