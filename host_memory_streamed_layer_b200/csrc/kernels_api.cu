@@ -173,6 +173,10 @@ extern "C" int mt_k_attn_bwd_tc(const void* q, const void* k, const void* v, int
 namespace {
 
 constexpr int kMostSize = 1 << 30;
+// Depth of a product. The tensor cores lose 1e-9 K of a sum that is rounded to
+// bf16: 1e-3 here, a quarter of the most that the rounding takes. And a tile's
+// main loop, whose end the epilogue awaits for at most a second, takes under 10 ms.
+constexpr int kMostDepth = 1 << 20;
 
 bool size_ok(int n) { return n >= 0 && n <= kMostSize; }
 bool type_ok(int t) { return t == MT_F32 || t == MT_BF16; }
@@ -250,6 +254,7 @@ extern "C" int mt_k_linear_fwd(const void* A, int64_t lda, const void* W, int64_
       !opt_mat_ok(R, out_type, ldr, N) || !opt_mat_ok(Z, MT_BF16, ldz, N) || !mat_ok(C, out_type, ldc, N) ||
       !al4(dev_err))
     return MT_ERR_ARG;
+  if (K > kMostDepth) return MT_ERR_CONFIG;
   const mt::LinearFwd a{A, lda, W, ldw, bias, act, R, ldr, Z, ldz, C, out_type, ldc, M, N, K};
   return mt::launch_linear_fwd(a, dd, S(stream), dev_err);
 }
@@ -270,6 +275,7 @@ extern "C" int mt_k_linear_bwd_act(const void* dY, int64_t lddy, const void* W, 
       !mat_ok(dZ, MT_BF16, lddz, N) || (act != MT_ACT_NONE && !Z) || (db && !part) || !al16(part) ||
       !al4(db, dev_err))
     return MT_ERR_ARG;
+  if (K > kMostDepth) return MT_ERR_CONFIG;
   const mt::LinearBwd a{dY, lddy, W, ldw, Z, ldz, act, dZ, lddz, part, db, M, N, K};
   return mt::launch_linear_bwd_act(a, dd, S(stream), dev_err);
 }
@@ -299,6 +305,7 @@ extern "C" int mt_k_gated_ffn_fwd(const void* x, int64_t ldx, const void* Wgu, i
   if (K == 0 || !mat_ok(x, MT_BF16, ldx, K) || !mat_ok(Wgu, MT_BF16, ldw, K) ||
       !opt_mat_ok(gu, MT_BF16, ldgu, 2 * (int64_t)F) || !mat_ok(h, MT_BF16, ldh, F) || !al4(dev_err))
     return MT_ERR_ARG;
+  if (K > kMostDepth) return MT_ERR_CONFIG;
   return mt::launch_gated_ffn_fwd(x, ldx, Wgu, ldw, act, gu, ldgu, h, ldh, M, F, K, S(stream), dev_err);
 }
 
@@ -311,5 +318,6 @@ extern "C" int mt_k_gated_ffn_bwd(const void* dy, int64_t lddy, const void* Wd, 
       !mat_ok(gu, MT_BF16, ldgu, 2 * (int64_t)F) || !mat_ok(dgu, MT_BF16, lddgu, 2 * (int64_t)F) ||
       !opt_mat_ok(h, MT_BF16, ldh, F) || !al4(dev_err))
     return MT_ERR_ARG;
+  if (K > kMostDepth) return MT_ERR_CONFIG;
   return mt::launch_gated_ffn_bwd(dy, lddy, Wd, ldw, gu, ldgu, act, dgu, lddgu, h, ldh, M, F, K, S(stream), dev_err);
 }

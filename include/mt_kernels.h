@@ -183,12 +183,14 @@ int mt_k_gemm_bf16_rope(const void* A, int64_t lda, const void* B, int64_t ldb, 
  *     once, to nearest even, from the fp32 result. The tensor cores truncate as
  *     they accumulate (a product of depth K comes out low by about 1e-9 K of
  *     itself, as in mt_k_gemm_bf16); fp32 outputs of these calls, C and db, are
- *     summed in pieces that keep that below 1e-6;
+ *     summed in pieces that keep that below 1e-6 (below 1.1e-6 at K = 2^20, where
+ *     the roundings of the pieces' additions show);
  *   - the calls are deterministic: the same inputs give the same bits;
  *   - buffers may not overlap unless a call allows it; scratch belongs to one
  *     call in flight at a time (calls that may run at once, captured graphs
  *     included, need scratch of their own);
- *   - rows, columns and depths up to 2^30;
+ *   - rows and columns up to 2^30, depths (K) up to 2^20 (MT_ERR_CONFIG
+ *     beyond);
  *   - the pointers and the stream belong to the current device.
  * ------------------------------------------------------------------------- */
 

@@ -3,7 +3,7 @@ the header states, each at the border: what lies behind it is refused on the
 host, before any device work (no GPU here)."""
 import pytest
 
-from test_block_ops_refusals import P, _mt, refused
+from test_block_ops_refusals import CONFIG, P, _mt, base, refused
 
 I64_MAX = (1 << 63) - 1
 
@@ -37,3 +37,22 @@ def test_vectors_off_their_elements_boundary_are_refused(name, vectors):
     for v in vectors:
         for off in (1, 2):
             refused(name, **{v: P() + off})
+
+
+DEEPEST = 1 << 20
+
+
+@pytest.mark.parametrize("name", ["mt_k_linear_fwd", "mt_k_linear_bwd_act", "mt_k_gated_ffn_fwd", "mt_k_gated_ffn_bwd"])
+@pytest.mark.parametrize("K", [DEEPEST + 1, 1 << 25, 1 << 30])
+def test_depths_behind_the_largest_are_refused(name, K):
+    """A product deeper than 2^20 would lose more than its output type rounds, and near 2^28 outlast its waits."""
+    pitches = {k: v for k, v in dict(lda=K, ldw=K, lddy=K, ldx=K).items() if k in base(name)}
+    if name in ("mt_k_linear_bwd_act", "mt_k_gated_ffn_bwd"):
+        del pitches["ldw"]  # W [K, N]
+    refused(name, CONFIG, K=K, **{k: (v + 7) // 8 * 8 for k, v in pitches.items()})
+
+
+def test_empty_products_of_any_depth_succeed():
+    mt = _mt()
+    mt.mt_k_linear_fwd(0, 0, 0, 0, 0, 0, None, 0, 0, 0, 0, 0, 0, 0, 0, 16, 1 << 30)
+    mt.mt_k_gated_ffn_fwd(0, 0, 0, 0, 4, 0, 0, 0, 0, 0, 16, 1 << 30)
