@@ -56,7 +56,7 @@ constexpr int EPI_WARPS = 8;
 // a sum comes out low by about 9.5e-10 K of itself. Beside a bf16 output's
 // rounding that is nothing, but fp32 outputs (a residual stream, the bias
 // gradient) would show it: 2e-6 at K = 2048, 6e-6 at 5504, where one in fp32
-// registers is off by under 1e-6. So from K = 960 on their kernels accumulate a
+// registers is off by under 1e-6. So from K = 897 on their kernels accumulate a
 // chunk of the k-blocks at a time and add the chunks in the epilogue warps'
 // registers (CHUNKED). Measured on one B200, interleaved, plain -> chunked: error
 // 6.0e-6 -> 8.6e-7 and 265 -> 293 us for dropout and an fp32 residual at 16333 x
@@ -942,22 +942,29 @@ LastWave last_wave(int rest, int n, bool mn_major) {
   return best;
 }
 
-// Chunks of n k-blocks. One of c loses 6.1e-8 c of itself, so n of them in
-// chunks c_i lose 6.1e-8 sum c_i^2 / n: at most 14.8 for 9e-7. The first two are
-// as long as that allows (up to 20), for the tensor cores have nothing but those
-// two to do while the epilogue warps finish the tile before; the rest have 12 at
-// most.
+// Chunks of the n k-blocks of a depth K, in stages of sub. One of c blocks loses up
+// to 7e-8 c of itself (measured), so chunks c_i lose 7e-8 sum c_i^2 / (K / 64): a
+// sum of 14.2 K / 64 at most keeps that below 1e-6. Up to 27 blocks that allows two
+// halves, of which none is a stub. Beyond, the first two are as long as it allows
+// (up to 20), for the tensor cores have nothing but those two to do while the
+// epilogue warps finish the tile before; the rest have 12 at most.
 struct Chunks {
   int first, rest;
 };
-Chunks chunks_of(int n) {
-  for (int first = n < 20 ? n : 20; first > 12; --first) {
+Chunks chunks_of(int K, int sub) {
+  const int n = (K + BK - 1) / BK;
+  if (n <= 27) {
+    const int half = ((n + 1) / 2 + sub - 1) / sub * sub;
+    return Chunks{half, half};
+  }
+  auto whole = [&](int c) { return c > sub ? c / sub * sub : sub; };
+  for (int first = 20; first > 12; --first) {
     const int left = n - 2 * first > 0 ? n - 2 * first : 0, second = n - first < first ? n - first : first;
     const int rest = left ? (left + (left + 11) / 12 - 1) / ((left + 11) / 12) : first;
     // left k-blocks in chunks of rest, the last one shorter
     const int full = left / rest, last = left - full * rest;
     const int lost = first * first + second * second + full * rest * rest + last * last;
-    if (10 * lost <= 148 * n) return Chunks{first, rest};
+    if (640 * (int64_t)lost <= 142 * (int64_t)K) return Chunks{whole(first), whole(rest)};
   }
   return Chunks{12, 12};
 }
@@ -983,9 +990,9 @@ int launch(Op o, int bn, int device, int num_sms, cudaStream_t st) {
   const int stage = p.t.sub * kb_bytes;
   // Without a bias gradient the backward's outputs are bf16 and need no chunks.
   if (CHUNKED) {  // multiples of sub, and num_kb > CHUNK_MOST
-    const Chunks c = chunks_of(num_kb);
-    p.t.chunk_first = c.first / p.t.sub * p.t.sub;
-    p.t.chunk_rest = c.rest > p.t.sub ? c.rest / p.t.sub * p.t.sub : p.t.sub;
+    const Chunks c = chunks_of(p.K, p.t.sub);
+    p.t.chunk_first = c.first;
+    p.t.chunk_rest = c.rest;
   }
   const int fit = (SMEM_MOST - 1024 - BAR_BYTES - epi) / stage;
   p.t.stages = fit < MAX_STAGES ? fit : MAX_STAGES;

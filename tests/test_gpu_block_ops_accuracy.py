@@ -1,4 +1,4 @@
-"""Accuracy of the products at the largest depth, against fp64."""
+"""Accuracy of the deep products, against fp64."""
 import pytest
 import torch
 
@@ -29,3 +29,24 @@ def test_products_at_the_largest_depth(out):
     want = A.double() @ W.double().T
     assert int(err) == 0
     assert far(C, want) <= float(want.norm()) * ((60 + 37) * 2.0 ** -24 if out == F32 else 2.0 ** -8 + 2.0 ** -8)
+
+
+@pytest.mark.parametrize("K", [897, 961, 1088, 1281, 1345, 1729, 1857, 2305, 5504])
+@pytest.mark.parametrize("M,N", [(512, 512), (40, 2048)])
+def test_fp32_outputs_stay_below_the_stated_loss(K, M, N):
+    """C and the bias gradient within 1e-6 of themselves (relative L2), as the
+    header says, where the accumulator is added up in two parts or a few."""
+    mt = _mt()
+    g = torch.Generator(device=DEV).manual_seed(K)
+    ld = (K + 7) // 8 * 8
+    A, W = (torch.zeros(n, ld, dtype=BF16, device=DEV) for n in (M, N))
+    A[:, :K], W[:, :K] = torch.randn(M, K, generator=g, device=DEV), torch.randn(N, K, generator=g, device=DEV)
+    Wk = W[:, :K].T.contiguous()
+    C, dZ, db = torch.zeros(M, N, device=DEV), torch.zeros(M, N, dtype=BF16, device=DEV), torch.zeros(N, device=DEV)
+    part = torch.zeros(mt.mt_k_linear_bwd_act_partial_floats(M, N), device=DEV)
+    mt.mt_k_linear_fwd(A.data_ptr(), ld, W.data_ptr(), ld, 0, 0, None, 0, 0, 0, 0, C.data_ptr(), 0, N, M, N, K, stream())
+    mt.mt_k_linear_bwd_act(A.data_ptr(), ld, Wk.data_ptr(), N, 0, 0, 0, None, dZ.data_ptr(), N, part.data_ptr(), db.data_ptr(), M,
+                           N, K, stream())
+    want = A.double() @ W.double().T
+    assert far(C, want) <= 1e-6 * float(want.norm())
+    assert far(db, want.sum(0)) <= 1e-6 * float(want.sum(0).norm())
