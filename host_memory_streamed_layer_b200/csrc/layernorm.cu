@@ -4,10 +4,14 @@
 //   dx_j = dres_j + r (w_j - mean w - xh_j mean(w xh))
 //   dg_j = sum over rows of dy_j xh_j,  db_j = sum over rows of dy_j.
 // Both passes are bound by device memory: each reads its inputs once, and the
-// row's two statistics are taken in fp32 (the variance from the centred values,
-// so that a large mean costs no digits). Measured on one B200: 16384 x 2048
-// fp32 to bf16 forward 37 us (5.4 TB/s), backward with the residual's gradient
-// and a bf16 copy 104 us (5.8 TB/s; a copy kernel reaches 6.5).
+// row's two statistics are taken in fp32. The forward's first mean is off by the
+// rounding of a sum of d values, a few 2^-24 of itself, which is much beside the
+// spread of a row whose mean is large. So the centred values t = x - m are summed
+// along with their squares: their mean s (nearly 0) is what m is off by, and
+//   mean = m + s,  variance = mean t^2 - s^2,  xh = (t - s) r,
+// where t itself is exact or nearly so. Measured on one B200: 16384 x 2048 fp32 to
+// bf16 forward 37 us (5.4 TB/s), backward with the residual's gradient and a bf16
+// copy 104 us (5.8 TB/s; a copy kernel reaches 6.5).
 #include "act_dropout.cuh"
 
 namespace mt {
@@ -39,6 +43,43 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, float* red) {
   return s;
 }
 
+// The same for one number; `red` has blockDim.x / 32 floats.
+template <int TX>
+__device__ __forceinline__ float row_sum(float a, float* red) {
+  a = warp_sum(a);
+  if (TX == 32) return a;
+  const int warp = threadIdx.x >> 5;
+  if ((threadIdx.x & 31) == 0) red[warp] = a;
+  __syncthreads();
+  constexpr int W = TX / 32;
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < W; ++i) s += red[warp / W * W + i];
+  return s;
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 c;
+  asm("{\n\t.reg .b64 x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 z, x, y;\n\t"
+      "mov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(c.x), "=f"(c.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return c;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 w, x, y, z;\n\t"
+      "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
+      "fma.rn.f32x2 z, x, y, w;\n\t"
+      "mov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
 // A lane reads W neighbouring columns at a time, 16 bytes of the wider of the
 // two types: with eight columns of an fp32 row to a lane, each access would
 // take only half of every sector that it touches.
@@ -66,41 +107,52 @@ __device__ __forceinline__ void load_piece(const T* p, int n, float (&v)[W]) {
 
 // Forward: TX threads to a row, G pieces of W columns to a thread: 32 columns
 // to a thread up to 4096, so that each has 64 bytes or more in flight (with 16
-// columns a bf16 row of 2048 took 32.8 us for 16384 rows instead of 29.6).
+// columns a bf16 row of 2048 took 32.8 us for 16384 rows instead of 29.6). The
+// arithmetic of two columns goes into one instruction: singly, the sum of t cost
+// 2 to 9 % (bf16 16384 x 2048 32.8 us instead of 28.7; 30.8 without that sum). Eight
+// columns to a thread leave room for eight blocks on an SM, 24 for five.
 template <typename X, typename Y, int TX, int G, bool EXACT, int W = piece<X, Y>()>
-__global__ void __launch_bounds__(256) k_layernorm_fwd(const X* __restrict__ x, int64_t ldx, const bf16* __restrict__ g,
-                                                       const bf16* __restrict__ b, Y* __restrict__ y, int64_t ldy,
-                                                       float* __restrict__ mean, float* __restrict__ rstd, int T, int d,
-                                                       float eps) {
+__global__ void __launch_bounds__(256, G * W <= 8 ? 8 : EXACT && G * W <= 24 ? 5 : 4)
+    k_layernorm_fwd(const X* __restrict__ x, int64_t ldx, const bf16* __restrict__ g, const bf16* __restrict__ b,
+                    Y* __restrict__ y, int64_t ldy, float* __restrict__ mean, float* __restrict__ rstd, int T, int d,
+                    float eps) {
   __shared__ float red[2][16];
   const int64_t row = (int64_t)blockIdx.x * (256 / TX) + threadIdx.x / TX;
   const int tx = threadIdx.x % TX;
   const bool ok = row < T;
   if (TX == 32 && !ok) return;  // a wider row's threads all stay for the barriers
   const X* xr = x + row * ldx;
+  const float inv_d = 1.f / (float)d;
   float v[G][W];
-  float s = 0.f;
 #pragma unroll
   for (int k = 0; k < G; ++k) {
     const int c = (tx + k * TX) * W;
     load_piece<W, EXACT>(xr + c, ok ? d - c : 0, v[k]);
   }
+  // Sums of the even and of the odd columns.
+  float2 s = make_float2(0.f, 0.f), u = s, q = s;
 #pragma unroll
   for (int k = 0; k < G; ++k)
 #pragma unroll
-    for (int e = 0; e < W; ++e) s += v[k][e];
-  const float m = row_sum2<TX>(s, 0.f, red[0]).x / (float)d;
-  float q = 0.f;
+    for (int e = 0; e < W; e += 2) s = add2(s, make_float2(v[k][e], v[k][e + 1]));
+  const float m = row_sum<TX>(s.x + s.y, red[0]) / (float)d;
 #pragma unroll
   for (int k = 0; k < G; ++k) {
     const int n = d - (tx + k * TX) * W;
+    const float off = n > 0 ? -m : 0.f;  // behind the row: t = 0
 #pragma unroll
-    for (int e = 0; e < W; ++e) {
-      const float t = (EXACT ? n > 0 : e < n) ? v[k][e] - m : 0.f;
-      q += t * t;
+    for (int e = 0; e < W; e += 2) {
+      const float2 t = add2(make_float2(v[k][e], v[k][e + 1]),
+                            EXACT ? make_float2(off, off) : make_float2(e < n ? -m : 0.f, e + 1 < n ? -m : 0.f));
+      u = add2(u, t);
+      q = fma2(t, t, q);
+      v[k][e] = t.x, v[k][e + 1] = t.y;
     }
   }
-  const float r = rsqrtf(row_sum2<TX>(q, 0.f, red[1]).x / (float)d + eps);
+  const float2 tu = row_sum2<TX>(u.x + u.y, q.x + q.y, red[1]);
+  const float shift = tu.x * inv_d, var = tu.y * inv_d - fminf(shift * shift, 3e38f);  // inf - inf: none
+  const float r = rsqrtf((var < 0.f ? 0.f : var) + eps);  // below 0 by rounding alone; NaN stays
+  const float minus = -shift * r;
 #pragma unroll
   for (int k = 0; k < G; ++k) {
     const int c = (tx + k * TX) * W;
@@ -114,11 +166,15 @@ __global__ void __launch_bounds__(256) k_layernorm_fwd(const X* __restrict__ x, 
       for (int e = 0; e < W; ++e) bv[e] = 0.f;
     }
 #pragma unroll
-    for (int e = 0; e < W; ++e) v[k][e] = (v[k][e] - m) * r * gv[e] + bv[e];
+    for (int e = 0; e < W; e += 2) {
+      const float2 xh = fma2(make_float2(v[k][e], v[k][e + 1]), make_float2(r, r), make_float2(minus, minus));
+      const float2 o = fma2(xh, make_float2(gv[e], gv[e + 1]), make_float2(bv[e], bv[e + 1]));
+      v[k][e] = o.x, v[k][e + 1] = o.y;
+    }
     store_n<W>(y + row * ldy + c, EXACT ? W : d - c, v[k]);
   }
   if (ok && tx == 0) {
-    if (mean) mean[row] = m;
+    if (mean) mean[row] = shift == shift ? m + shift : m;  // an infinite mean stays one
     if (rstd) rstd[row] = r;
   }
 }

@@ -234,7 +234,8 @@ typedef struct mt_dropout {
  *   y_j = (x_j - m) r g_j + b_j.
  * x [T, d] of x_type, y [T, d] of y_type; g, b bf16 [d] (b NULL: no shift);
  * mean, rstd fp32 [T] (each may be NULL) receive m and r, which the backward
- * reads. eps >= 0; d <= 8192 (MT_ERR_CONFIG otherwise). */
+ * reads. y does not lose digits to a mean that is large beside the row's spread;
+ * m is saved rounded to fp32. eps >= 0; d <= 8192 (MT_ERR_CONFIG otherwise). */
 int mt_k_layernorm_fwd(const void* x, int x_type, int64_t ldx, const void* g, const void* b, void* y, int y_type,
                        int64_t ldy, float* mean, float* rstd, int T, int d, float eps, void* stream);
 

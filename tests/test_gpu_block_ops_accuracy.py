@@ -1,13 +1,84 @@
-"""Accuracy of the deep products, against fp64."""
+"""Accuracy of the layer-norm and linear kernels where a plain tolerance would
+hide a loss: rows whose mean is far larger than their spread, and deep
+products. References are fp64."""
+import numpy as np
 import pytest
 import torch
 
-from test_gpu_block_ops import DEV, _mt, stream
+from oracle import block
+from test_gpu_block_ops import CHAIN, DEV, HALF, Mat, _mt, np64, scratch, stream, vec, within
 
 pytestmark = pytest.mark.gpu
 F32, BF16 = torch.float32, torch.bfloat16
 
 
+# ---------------------------------------------------------------------------
+# Layer norm of rows with a large mean
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("T,d", [(4, 3), (9, 257), (6, 1000), (37, 2048), (11, 2049), (5, 5120), (3, 8192)])
+@pytest.mark.parametrize("times,xt", [(1e3, F32), (-1e4, F32), (1e5, F32), (100.0, BF16)])
+@pytest.mark.parametrize("yt", [F32, BF16])
+def test_layernorm_fwd_of_rows_with_a_large_mean(T, d, times, xt, yt):
+    """A mean of `times` the spread. A first mean m, off by e <= CHAIN |mean|,
+    shifts t = x - m, which is exact or off by 2^-24 of itself; the mean of t
+    then takes the shift out, off by CHAIN mean |t| <= CHAIN (a + e) with a the
+    mean of |x - mean|. So the bound on y grows with e^2 at most, not with the
+    mean. The variance mean t^2 - shift^2 is off by CHAIN (var + e^2)."""
+    mt = _mt()
+    rng = np.random.default_rng(T + d)
+    x = Mat(T, d, xt, 1.5 * rng.normal(size=(T, d)) + 1.5 * times * (1 + 0.1 * rng.normal(size=(T, 1))))
+    g, b = vec(1 + 0.1 * rng.normal(size=d), BF16), vec(0.3 * rng.normal(size=d), BF16)
+    y, m, r = Mat(T, d, yt), scratch(T), scratch(T)
+    mt.mt_k_layernorm_fwd(x.ptr, x.kind, x.ld, g.data_ptr(), b.data_ptr(), y.ptr, y.kind, y.ld, m.data_ptr(), r.data_ptr(), T, d,
+                          1e-5, stream())
+    X, G, B = x.np(), np64(g), np64(b)
+    want, wm, wr = block.layernorm_fwd(X, G, B, 1e-5)
+    a, e = np.abs(X - wm[:, None]).mean(axis=1), CHAIN * np.abs(wm)
+    shift = CHAIN * (a + e)
+    spread = CHAIN * (1 + (e * wr) ** 2) + 2.0 ** -21  # of r, relative: half the variance's, and rsqrt's
+    within(np64(m)[:T], wm, 2.0 ** -24 * np.abs(wm) * 1.001 + shift)
+    within(np64(r)[:T], wr, spread * wr)
+    xh = np.abs(X - wm[:, None]) * wr[:, None]
+    tol = HALF[yt] * np.abs(want) + np.abs(G) * ((shift * wr)[:, None] + xh * spread[:, None]) + \
+        4 * 2.0 ** -24 * (xh * np.abs(G) + np.abs(B))
+    within(y.np(), want, tol)
+
+
+@pytest.mark.parametrize("value", [0.1, -1234.567, 3.3e7])
+@pytest.mark.parametrize("d", [3, 515, 2048, 5120])
+def test_layernorm_fwd_of_a_constant_row(value, d):
+    """x - mean is 0 whatever the value's digits: y is b up to the shift's own
+    rounding (at most CHAIN of a shift of CHAIN |value|, times r = eps^-1/2)."""
+    mt = _mt()
+    x, y = Mat(2, d, F32, np.full((2, d), value)), Mat(2, d, F32)
+    rng = np.random.default_rng(d)
+    g, b = vec(1 + 0.1 * rng.normal(size=d), BF16), vec(0.3 * rng.normal(size=d), BF16)
+    mt.mt_k_layernorm_fwd(x.ptr, 0, x.ld, g.data_ptr(), b.data_ptr(), y.ptr, 0, y.ld, 0, 0, 2, d, 1e-5, stream())
+    want = np.broadcast_to(np64(b), (2, d))
+    within(y.np(), want, np.abs(np64(g)) * CHAIN ** 2 * abs(value) * 1e-5 ** -0.5 + 2.0 ** -22 * np.abs(want))
+
+
+def test_layernorm_fwd_statistics_of_rows_that_are_not_finite():
+    """The mean of a row with infinities of one sign is that infinity, of one with
+    a NaN NaN; a row whose digits' squares are beyond fp32 stays finite."""
+    mt = _mt()
+    T, d = 6, 300
+    x = np.ones((T, d))
+    x[0, 7], x[1, 0], x[2, 299], x[3, :] = np.inf, -np.inf, np.nan, 1e27
+    X, y = Mat(T, d, F32, x), Mat(T, d, F32)
+    g, b = vec(np.ones(d), BF16), vec(np.full(d, 0.5), BF16)
+    m, r = scratch(T), scratch(T)
+    mt.mt_k_layernorm_fwd(X.ptr, 0, X.ld, g.data_ptr(), b.data_ptr(), y.ptr, 0, y.ld, m.data_ptr(), r.data_ptr(), T, d, 1e-5,
+                          stream())
+    got, mean = y.np(), np64(m)
+    assert mean[0] == np.inf and mean[1] == -np.inf and np.isnan(mean[2]) and np.isnan(mean[T])
+    assert np.isnan(got[:3]).all() and (got[4:] == 0.5).all()
+    assert np.isfinite(got[3]).all()
+
+
+# ---------------------------------------------------------------------------
+# Deep products
+# ---------------------------------------------------------------------------
 def far(got, want):
     return float((got.double() - want).norm())
 
