@@ -106,7 +106,10 @@ __device__ __forceinline__ void act_bwd_rows(const X* dc, int64_t lddc, const bf
     if (!WHOLE && t >= end) break;
     if (ACT != MT_ACT_NONE) {
 #pragma unroll
-      for (int e = 0; e < W; ++e) v[i][e] *= act_slope<ACT>(zv[i][e]);
+      for (int e = 0; e < W; e += 2) {
+        const float2 slope = act_slope<ACT>(make_float2(zv[i][e], zv[i][e + 1]));
+        v[i][e] *= slope.x, v[i][e + 1] *= slope.y;
+      }
     }
     // last, so that a dropped element is 0 whatever dc and z hold there
     if (drop.on) drop_piece<W>(v[i], c, drop.row0 + (uint32_t)t, drop, key);

@@ -300,7 +300,10 @@ __device__ __forceinline__ void linear_block(const Params& p, const DropKey& key
 #pragma unroll
   for (int i = 0; i < NR; ++i)
 #pragma unroll
-    for (int e = 0; e < NC; ++e) v[i][e] = act_value<ACT>(v[i][e]);
+    for (int e = 0; e < NC; e += 2) {
+      const float2 a2 = act_value<ACT>(make_float2(v[i][e], v[i][e + 1]));
+      v[i][e] = a2.x, v[i][e + 1] = a2.y;
+    }
   if (p.drop.on) drop_rows<EPI>(p, key, row0, col, v);
   if (p.R) {
 #pragma unroll
@@ -331,7 +334,10 @@ __device__ __forceinline__ void bwd_block(const Params& p, const DropKey& key, i
       float t[8];
       unpack8(a.x[i], t);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] *= act_slope<ACT>(t[e]);
+      for (int e = 0; e < 8; e += 2) {
+        const float2 slope = act_slope<ACT>(make_float2(t[e], t[e + 1]));
+        v[i][e] *= slope.x, v[i][e + 1] *= slope.y;
+      }
     }
   }
   if (p.drop.on) drop_rows<E_BWD>(p, key, row0, col, v);  // last: a dropped element is 0 whatever Z holds there
@@ -371,12 +377,12 @@ __device__ __forceinline__ void gated_bwd_block(const Params& p, int row0, int c
     unpack8(a.x[2 * i], g);
     unpack8(a.x[2 * i + 1], u);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float value, slope;
-      act_both<ACT>(g[e], value, slope);
-      h[e] = value * u[e];
-      g[e] = v[i][e] * u[e] * slope;
-      u[e] = v[i][e] * value;
+    for (int e = 0; e < 8; e += 2) {
+      float2 value, slope;
+      act_both<ACT>(make_float2(g[e], g[e + 1]), value, slope);
+      h[e] = value.x * u[e], h[e + 1] = value.y * u[e + 1];
+      g[e] = v[i][e] * u[e] * slope.x, g[e + 1] = v[i][e + 1] * u[e + 1] * slope.y;
+      u[e] = v[i][e] * value.x, u[e + 1] = v[i][e + 1] * value.y;
     }
     bf16* o = p.dgu + row * p.lddgu + col;
     store8(o, g);
@@ -422,7 +428,10 @@ __device__ __forceinline__ void gated_block(const Params& p, int row0, int col, 
     __syncwarp();
   }
 #pragma unroll
-  for (int e = 0; e < 32; ++e) v[e] = act_value<ACT>(__uint_as_float(a[e])) * __uint_as_float(b[e]);
+  for (int e = 0; e < 32; e += 2) {
+    const float2 h = act_value<ACT>(make_float2(__uint_as_float(a[e]), __uint_as_float(a[e + 1])));
+    v[e] = h.x * __uint_as_float(b[e]), v[e + 1] = h.y * __uint_as_float(b[e + 1]);
+  }
   stage_bf16(st, lane, v);
   __syncwarp();
 #pragma unroll

@@ -15,11 +15,11 @@ import math
 import numpy as np
 
 ACTS = ("none", "relu", "gelu", "gelu_tanh", "silu")
-_erf = np.frompyfunc(math.erf, 1, 1)
+_erfc = np.frompyfunc(math.erfc, 1, 1)
 
 
 def _normal_cdf(z):
-    return 0.5 * (1.0 + _erf(np.asarray(z, dtype=np.float64) / math.sqrt(2.0)).astype(np.float64))
+    return 0.5 * _erfc(np.asarray(z, dtype=np.float64) / -math.sqrt(2.0)).astype(np.float64)  # the lower tail keeps its digits
 
 
 def act(z, kind):

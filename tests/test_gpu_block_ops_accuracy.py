@@ -1,6 +1,9 @@
 """Accuracy of the layer-norm and linear kernels where a plain tolerance would
-hide a loss: rows whose mean is far larger than their spread, and deep
-products. References are fp64."""
+hide a loss: rows whose mean is far larger than their spread, the lower tails
+of the activations, and deep products. References are fp64, written so that they
+keep their own digits there."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -74,6 +77,60 @@ def test_layernorm_fwd_statistics_of_rows_that_are_not_finite():
     assert mean[0] == np.inf and mean[1] == -np.inf and np.isnan(mean[2]) and np.isnan(mean[T])
     assert np.isnan(got[:3]).all() and (got[4:] == 0.5).all()
     assert np.isfinite(got[3]).all()
+
+
+# ---------------------------------------------------------------------------
+# The activations' lower tails
+# ---------------------------------------------------------------------------
+def gelu_parts(z):
+    cdf = np.array([0.5 * math.erfc(-v / math.sqrt(2)) for v in z])
+    return cdf, np.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+
+
+def value_slope(z, act):
+    """Value, slope, the size of the slope's terms, and the relative error that a
+    term may have, in units of 2^-24. A hardware reciprocal or power of two is
+    off by 4 units, a polynomial of a few terms by 8; a power's argument is off
+    by a rounding or two of itself, which counts as many units as it is large:
+    1.1 z^2 for exp(-z^2 / 2), |z| and 4 |u| (u itself takes three roundings) for the
+    two logistic forms."""
+    if act == "gelu":
+        cdf, pdf = gelu_parts(z)
+        return z * cdf, cdf + z * pdf, cdf + np.abs(z) * pdf, 16 + 1.1 * z * z
+    if act == "silu":
+        s, w = 1 / (1 + np.exp(-z)), 1 / (1 + np.exp(z))
+        return z * s, s * (1 + z * w), s * (1 + np.abs(z) * w), 16 + 1.5 * np.abs(z)
+    k = math.sqrt(8 / math.pi)
+    u = k * (z + 0.044715 * z ** 3)
+    s, w = 1 / (1 + np.exp(-u)), 1 / (1 + np.exp(u))
+    du = k * (1 + 3 * 0.044715 * z * z)
+    return z * s, s * (1 + z * w * du), s * (1 + np.abs(z) * w * du), 16 + 4 * np.abs(u)
+
+
+@pytest.mark.parametrize("act,low", [("gelu", -12.5), ("gelu_tanh", -9.0), ("silu", -80.0)])
+def test_activation_tails_keep_their_digits(act, low):
+    """Value (fp32 output of a product by the identity) and slope (the bias
+    gradient of one row, which is not rounded) on every bf16 number of the lower
+    tail down to where the power of two leaves the normal numbers, relative to
+    the value itself; and the value on the upper side."""
+    mt = _mt()
+    z = torch.arange(0, 1 << 15, dtype=torch.int32).to(torch.int16).view(BF16).double().numpy()
+    z = z[(z >= 2.0 ** -10) & (z <= -low)]
+    neg, both = -z, np.concatenate([-z, z])
+    kind = block.ACTS.index(act)
+    n = len(both)
+    A, W = Mat(1, 8, BF16, np.eye(1, 8)), Mat(n, 8, BF16, both[:, None] * np.eye(1, 8))
+    C = Mat(1, n, F32)
+    mt.mt_k_linear_fwd(A.ptr, A.ld, W.ptr, W.ld, 0, kind, None, 0, 0, 0, 0, C.ptr, 0, C.ld, 1, n, 8, stream())
+    value, _, _, units = value_slope(both, act)
+    within(C.np()[0], value, units * 2.0 ** -24 * np.abs(value))
+    n = len(neg)
+    _, slope, terms, units = value_slope(neg, act)
+    dC, Z, dZ, db = Mat(1, n, F32, np.ones((1, n))), Mat(1, n, BF16, neg[None]), Mat(1, n, BF16), scratch(n)
+    part = scratch(mt.mt_k_act_bwd_partial_floats(1, n))
+    mt.mt_k_act_bwd(dC.ptr, 0, dC.ld, Z.ptr, Z.ld, kind, None, dZ.ptr, dZ.ld, part.data_ptr(), db.data_ptr(), 1, n, stream())
+    within(np64(db)[:n], slope, (units + 4) * 2.0 ** -24 * terms)
+    within(dZ.np()[0], slope, 2.0 ** -8 * np.abs(slope) + (units + 4) * 2.0 ** -24 * terms)
 
 
 # ---------------------------------------------------------------------------
