@@ -9,7 +9,7 @@ import pytest
 import torch
 
 from oracle import block
-from test_gpu_block_ops import CHAIN, DEV, HALF, Mat, _mt, np64, scratch, stream, vec, within
+from test_gpu_block_ops import CHAIN, DEV, HALF, OFFSET, SEED, Mat, _mt, np64, scratch, stream, vec, within
 
 pytestmark = pytest.mark.gpu
 F32, BF16 = torch.float32, torch.bfloat16
@@ -138,6 +138,69 @@ def test_activation_tails_keep_their_digits(act, low):
 # ---------------------------------------------------------------------------
 def far(got, want):
     return float((got.double() - want).norm())
+
+
+@pytest.mark.parametrize("M,N,K", [(2309, 1948, 5504), (4000, 1300, 5000), (70, 1300, 5504)])
+@pytest.mark.parametrize("fam", [0, 1, 2])
+def test_fp32_outputs_of_deep_products_with_everything_in_the_epilogue(M, N, K, fam):
+    """Bias, ReLU, dropout, fp32 residual and Z forward; slope, dropout and bias
+    gradient back; at depths whose accumulator is added up in parts, on more
+    full-width pair tiles than there are pairs (the rest cut) and on few rows.
+
+    A part of at most 15 k-blocks on average takes 60 steps that each truncate
+    half a unit, 2^-24, on average: 60 x 2^-24 of the product (relative L2). All
+    344 steps of K = 5504 at once would lose 6e-6. The epilogue adds the roundings
+    of the bias, the scale and the residual, 2^-24 each of what they round."""
+    mt = _mt()
+    g = torch.Generator(device=DEV).manual_seed(M + K)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV)  # noqa: E731
+    ld, p, unit = (N + 7) // 8 * 8 + 8, 0.25, 2.0 ** -24
+    A, W, bias = r(M, K).bfloat16(), (r(N, K) / K ** 0.5).bfloat16(), (0.3 * r(N)).bfloat16()
+    R, C = r(M, ld), torch.full((M + 1, ld), 77.0, device=DEV)
+    Z = torch.full((M + 1, ld), 77.0, dtype=BF16, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    drop = mt.mt_dropout(p, SEED, OFFSET, 0, 3)
+    keep = torch.from_numpy(block.dropout_keep(M, N, p, SEED, OFFSET, 3)).to(DEV)
+    was = mt.mt_k_gemm_variant(fam)
+    try:
+        mt.mt_k_linear_fwd(A.data_ptr(), K, W.data_ptr(), K, bias.data_ptr(), mt.MT_ACT_RELU, drop, R.data_ptr(), ld, Z.data_ptr(),
+                           ld, C.data_ptr(), 0, ld, M, N, K, stream(), err.data_ptr())
+        torch.cuda.synchronize()
+        assert int(err) == 0
+        product = A.double() @ W.double().T
+        U = product + bias.double()
+        kept = keep & (U > 0)
+        D = torch.where(keep, U.clamp(min=0) / (1 - p), 0.0)
+        want = R[:, :N].double() + D
+        got = C[:M, :N]
+        assert torch.equal(got[~keep], R[:, :N][~keep])  # what is dropped leaves the residual as it is
+        lost = 60 * unit * float((product * kept).norm()) / (1 - p)
+        assert far(got, want) <= lost + unit * float(2 * D.norm() + want.norm())
+        assert bool(((Z[:M, :N].double() - U).abs() <= 2.0 ** -8 * U.abs() +
+                     (K / 16 + 16) * 2.0 ** -23 * (A.double().abs() @ W.double().abs().T)).all())
+        for t in (C, Z):
+            assert bool((t[:, N:] == 77).all()) and bool((t[M] == 77).all())
+        # back: the same depth, GELU's slope at a Z of its own
+        Wk, zb = torch.zeros(K, ld, dtype=BF16, device=DEV), (1.5 * r(M, ld)).bfloat16()
+        Wk[:, :N] = W.T
+        dZ = torch.full((M + 1, ld), 77.0, dtype=BF16, device=DEV)
+        part, db = scratch(mt.mt_k_linear_bwd_act_partial_floats(M, N)), scratch(N)
+        mt.mt_k_linear_bwd_act(A.data_ptr(), K, Wk.data_ptr(), ld, zb.data_ptr(), ld, mt.MT_ACT_GELU, drop, dZ.data_ptr(), ld,
+                               part.data_ptr(), db.data_ptr(), M, N, K, stream(), err.data_ptr())
+        torch.cuda.synchronize()
+    finally:
+        mt.mt_k_gemm_variant(was)
+    assert int(err) == 0
+    z = zb[:, :N].double()
+    slope = torch.special.ndtr(z) + z * torch.exp(-z * z / 2) / math.sqrt(2 * math.pi)
+    want = torch.where(keep, product * slope / (1 - p), 0.0)
+    assert bool((dZ[:M, :N][~keep] == 0).all()) and bool((dZ[:, N:] == 77).all()) and bool((dZ[M] == 77).all())
+    # dZ: rounded by 2^-8 at most, and by 2^-8 / sqrt 3 rms; the rest is far below
+    assert far(dZ[:M, :N], want) <= 2.0 ** -8 * float(want.norm())
+    # db: the product's loss is the same share of every term; the terms' own roundings (slope within 16 units, scale) and
+    # the additions (32 rows, then up to 32 chains) are random
+    assert far(db[:N], want.sum(0)) <= 60 * unit * float(want.sum(0).norm()) + 16 * unit * float(want.norm())
+    assert bool(torch.isnan(db[N])) and bool(torch.isnan(part[-1]))
 
 
 @pytest.mark.parametrize("out", [F32, BF16])
