@@ -82,14 +82,6 @@ __device__ __forceinline__ void store_n(T* p, int n, const float (&v)[W]) {
       if (e < n) put(p + e, v[e]);
   }
 }
-template <typename T>
-__device__ __forceinline__ void load8n(const T* p, int n, float (&v)[8]) {
-  load_n<8>(p, n, v);
-}
-template <typename T>
-__device__ __forceinline__ void store8n(T* p, int n, const float (&v)[8]) {
-  store_n<8>(p, n, v);
-}
 
 // ---------------------------------------------------------------------------
 // Activations, in fp32. With Phi the logistic function or the normal

@@ -124,7 +124,9 @@ __global__ void __launch_bounds__(256, 4) k_act_bwd(const X* dc, int64_t lddc, c
                                                  const DropDesc drop, bf16* dz, int64_t lddz, float* __restrict__ part,
                                                  int M, int N, int rows_per_block, int tx_log2) {
   __shared__ float sh[256 * W];
-  let_next_start();  // every block of this kernel is resident from the start
+  // The column sums' kernel starts once every block of this one has, so it takes
+  // no room from them; up to 592 column strips they are all resident at once.
+  let_next_start();
   const int TX = 1 << tx_log2, tx = threadIdx.x & (TX - 1), ty = threadIdx.x >> tx_log2, ry = 256 >> tx_log2;
   const int c = (((int)blockIdx.x << tx_log2) + tx) * W;
   const int n = N - c;
@@ -184,7 +186,7 @@ Grid grid_for(int rows, int cols, int w, int blocks) {
 // 84 us on 8192 x 5120 with a residual, 32 take 74).
 constexpr int kDropoutBlocks = 148 * 32;
 // The backward's blocks each leave a row of partial column sums, so there are
-// only as many as run at once.
+// only as many as run at once (one to each strip of columns at least).
 constexpr int kActBwdBlocks = 148 * 4;
 
 template <typename X, typename Y>

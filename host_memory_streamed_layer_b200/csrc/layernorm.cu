@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(LnBwd<X, Y, TX, G>::THREADS, LnBwd<X, Y, TX, G
   using L = LnBwd<X, Y, TX, G>;
   constexpr int W = L::W, RY = L::RY, S = L::STAGES;
   extern __shared__ __align__(16) uint8_t ring[];
-  let_next_start();  // every block of this kernel is resident from the start
+  let_next_start();  // the column sums' kernel; every block of this one is resident from the start
   __shared__ float red[2][L::THREADS / 16];
   const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
   float ag[G][W], ab[G][W], gv[G][W];

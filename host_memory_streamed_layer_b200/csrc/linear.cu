@@ -189,7 +189,7 @@ struct Aux {
 __device__ __forceinline__ uint4 load8_raw(const bf16* p, int n) {
   if (n >= 8) return *reinterpret_cast<const uint4*>(p);
   float t[8];
-  load8n(p, n, t);
+  load_n<8>(p, n, t);
   return pack8(t);
 }
 
@@ -481,7 +481,7 @@ __global__ void __launch_bounds__(Warps<CHUNKED>::THREADS, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  if (EPI == E_BWD) let_next_start();  // the column sums' kernel; this one's blocks are all resident
+  if (EPI == E_BWD) let_next_start();  // the column sums' kernel, which starts once all of these blocks have
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0;
