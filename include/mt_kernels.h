@@ -185,9 +185,10 @@ int mt_k_gemm_bf16_rope(const void* A, int64_t lda, const void* B, int64_t ldb, 
  *     itself, as in mt_k_gemm_bf16); fp32 outputs of these calls, C and db, are
  *     summed in pieces that keep that below 1e-6 (below 1.1e-6 at K = 2^20, where
  *     the roundings of the pieces' additions show);
- *   - an activation, and each term of its slope, is within 4e-6 of itself for
- *     |z| <= 4 and within 2e-5 in the far lower tails, down to where exp(z),
- *     exp(-z^2 / 2) or their like falls below 2^-126 and counts as 0;
+ *   - an activation is within 4e-6 of itself for |z| <= 4 and within 2e-5 in the
+ *     far lower tails, down to where exp(z), exp(-z^2 / 2) or their like falls
+ *     below 2^-126 and counts as 0; its slope, Phi + z Phi' with Phi the
+ *     distribution function behind it, within the same shares of |Phi| + |z Phi'|;
  *   - the calls are deterministic: the same inputs give the same bits;
  *   - buffers may not overlap unless a call allows it; scratch belongs to one
  *     call in flight at a time (calls that may run at once, captured graphs
